@@ -381,6 +381,147 @@ svdq_status svdq_fold_scale(const void* x, svdq_dtype x_dtype, int64_t B, int64_
 
 svdq_status svdq_fold_scale_workspace_size(int64_t B, int64_t M, size_t* bytes);
 
+/*
+ * Attention between two linears.
+ *
+ * A transformer layer whose projections are svdq_linear calls needs, between the
+ * qkv projection and the output projection: an RMS norm of each query and key
+ * head, the rotation by position, a cache of keys and values, and attention. The
+ * calls below read the heads where svdq_linear wrote them (a row q | k | v of the
+ * projection is three strided tensors) and write the rows the next svdq_linear
+ * reads. All are inference operators (no backward pass, like the linear).
+ */
+
+/* A [tokens, heads, head_dim] tensor: element (t, h, i) at
+ * data + t * token_ld + h * head_ld + i (strides in elements). data must be 16-byte
+ * aligned and both strides multiples of 16 bytes; head_ld >= head_dim, token_ld >= head_dim. */
+typedef struct svdq_heads {
+  void* data;
+  int64_t token_ld, head_ld;
+  int32_t heads;
+} svdq_heads;
+
+/* Rotary positions. Pair j (0 <= j < rot_dim / 2) of a head at position p turns by
+ * the angle 2 pi p turns[j]:
+ *   (a, b) -> amplitude * (a cos - b sin, b cos + a sin)
+ * with (a, b) = elements (j, j + rot_dim/2) of the head, or (2j, 2j + 1) when
+ * interleaved; elements >= rot_dim pass through. The product p turns[j] is reduced to
+ * one turn in fp64, so far positions lose nothing. turns holds the frequencies in
+ * turns per position (base^(-2j/rot_dim) / (2 pi), scaled for long contexts as the
+ * model asks; amplitude is that scaling's attention factor, else 1). */
+typedef struct svdq_rope {
+  const double* turns;   /* device fp64 [rot_dim / 2]; may be NULL when rot_dim = 0 */
+  int32_t rot_dim;       /* even, 0 .. head_dim; 0: no rotation */
+  int32_t interleaved;   /* 0 or 1 */
+  float amplitude;       /* finite */
+} svdq_rope;
+
+/* A paged cache of bf16 keys and values: slot s of the cache is row s % page_size of
+ * page s / page_size; element (page, row, head, i) of k and of v at
+ * page * page_ld + row * slot_ld + head * head_ld + i. Any order of the three outer axes
+ * (rows of pages first or heads first) is a choice of strides. k and v are 16-byte
+ * aligned, the strides multiples of 8 elements. */
+typedef struct svdq_kv_cache {
+  void* k;
+  void* v;
+  int64_t pages;
+  int64_t page_ld, slot_ld, head_ld;
+  int32_t page_size, heads, head_dim;
+} svdq_kv_cache;
+
+/*
+ * svdq_qk_norm_rope - RMS norm and rotation of every query and key head, in one pass:
+ *   y = x * rsqrt(mean(x^2) + eps) * weight (when a weight is given), then the rotation.
+ * fp32 arithmetic, one rounding at the end.
+ *
+ *   q, k       [tokens, heads, head_dim] bf16 or fp32 (either may have data = NULL and
+ *              heads = 0); head_dim a multiple of 8, at most 256
+ *   positions  device int64 [tokens], any sign (may be NULL when rot_dim = 0)
+ *   q_weight, k_weight  device [head_dim], bf16 or fp32 (weight_dtype), 16-byte aligned;
+ *              NULL: no norm of these heads
+ *   q_out, k_out  outputs of the same type and sizes. An output may be its input
+ *              (same data and strides); otherwise it must not overlap any input.
+ * Host errors: SVDQ_EINVAL for null pointers, sizes, eps < 0 or not finite, and types;
+ * SVDQ_EUNSUPPORTED for head_dim or alignment outside the limits above.
+ */
+svdq_status svdq_qk_norm_rope(svdq_heads q, svdq_heads k, svdq_dtype dtype, int64_t tokens, int32_t head_dim,
+                              const int64_t* positions, svdq_rope rope, const void* q_weight,
+                              const void* k_weight, svdq_dtype weight_dtype, float eps, svdq_heads q_out,
+                              svdq_heads k_out, svdq_stream_t stream);
+
+/*
+ * svdq_kv_append - appends keys and values to a paged cache, with the norm and the
+ * rotation of svdq_qk_norm_rope applied to the keys on the way, and to the queries of
+ * the same tokens in the same pass. Everything is bf16.
+ *
+ *   k, v       [tokens, cache->heads, cache->head_dim]
+ *   slots      device int64 [tokens]: token t goes to that slot of the cache. Negative:
+ *              the token is padding and nothing of the cache is written for it (its
+ *              query and k_out rows are still computed). A slot >= pages * page_size
+ *              writes nothing and records SVDQ_EINVAL in the status word. Two tokens
+ *              must not name the same slot.
+ *   q, q_out   queries of the same tokens; data = NULL and heads = 0: none
+ *   k_out      the finished keys once more, for attention over the prompt itself;
+ *              data = NULL: not wanted. May be k (same data and strides).
+ * Slots that no token names keep their contents. Other arguments, aliasing and errors
+ * as in svdq_qk_norm_rope; the cache must not overlap any other tensor.
+ */
+svdq_status svdq_kv_append(const svdq_kv_cache* cache, svdq_heads k, svdq_heads v, const int64_t* slots,
+                           int64_t tokens, const int64_t* positions, svdq_rope rope, const void* k_weight,
+                           svdq_dtype weight_dtype, float eps, svdq_heads q, const void* q_weight,
+                           svdq_heads q_out, svdq_heads k_out, svdq_stream_t stream);
+
+/*
+ * svdq_attention_prompt - attention over whole prompts: packed sequences of different
+ * lengths, grouped heads, causal or full.
+ *   out[t, h] = sum_j p_j v[j, h / g] / sum_j p_j,  p_j = exp(scale q[t, h] . k[j, h / g])
+ * over the keys j of t's sequence, g = q.heads / k.heads. Everything is bf16; products
+ * and sums are fp32, and p is rounded to bf16 for its product with v.
+ *
+ *   q          [q_tokens, heads, head_dim];  k, v  [k_tokens, kv_heads, head_dim]
+ *              heads a multiple of kv_heads; head_dim a multiple of 8, at most 128
+ *   cu_q, cu_k device int32 [batch + 1]: sequence s owns rows cu[s] .. cu[s + 1] - 1;
+ *              either may be NULL with batch = 1: one sequence of all rows
+ *              (cu[0] >= 0, never decreasing, cu[batch] <= tokens). Entries that break
+ *              this record SVDQ_EINVAL in the status word; nothing outside the tensors is
+ *              read or written then, but the rows of the call have no meaning.
+ *   causal     1: row i of a sequence of n rows and m keys sees keys 0 .. m - n + i
+ *              (rows and keys end together); 0: all keys
+ *   scale      finite, e.g. 1 / sqrt(head_dim)
+ *   out        [q_tokens, heads, head_dim], must not overlap an input. A row that sees
+ *              no key becomes zero. Rows of no sequence are left as they were.
+ * Host errors: SVDQ_EINVAL, SVDQ_EUNSUPPORTED (head_dim, alignment; q_tokens,
+ * k_tokens, batch over 2^24, heads * (q_tokens / 64 + batch) over 2^30).
+ */
+svdq_status svdq_attention_prompt(svdq_heads q, svdq_heads k, svdq_heads v, const int32_t* cu_q,
+                                  const int32_t* cu_k, int32_t batch, int64_t q_tokens, int64_t k_tokens,
+                                  int32_t head_dim, int32_t causal, float scale, svdq_heads out,
+                                  svdq_stream_t stream);
+
+/*
+ * svdq_attention_decode - attention of one new token per sequence over a paged cache
+ * (which already holds that token: svdq_kv_append comes first). Formula and types of
+ * svdq_attention_prompt.
+ *
+ *   q, out     [batch, heads, head_dim], heads a multiple of cache->heads; cache->head_dim
+ *              a multiple of 8, at most 128
+ *   page_table device int32 [batch, table_ld] rows of page numbers; sequence s reads
+ *              page_table[s][0 .. ceil(kv_len[s] / page_size) - 1]. A number outside
+ *              [0, pages) records SVDQ_EINVAL and its keys are left out.
+ *   kv_len     device int32 [batch]; 0: the output row is zero. A length below 0 or over
+ *              table_ld * page_size records SVDQ_EINVAL and is read as 0 or that limit.
+ *   workspace  svdq_attention_decode_workspace_size bytes (16-byte aligned)
+ * The split of the work depends on the lengths alone, so results repeat bit for bit.
+ * Host errors: SVDQ_EINVAL, SVDQ_EUNSUPPORTED (head_dim, alignment), SVDQ_EWORKSPACE.
+ */
+svdq_status svdq_attention_decode(svdq_heads q, const svdq_kv_cache* cache, const int32_t* page_table,
+                                  int64_t table_ld, const int32_t* kv_len, int32_t batch, float scale,
+                                  svdq_heads out, void* workspace, size_t workspace_bytes,
+                                  svdq_stream_t stream);
+
+svdq_status svdq_attention_decode_workspace_size(int32_t batch, int32_t heads, int32_t kv_heads,
+                                                 int32_t head_dim, size_t* bytes);
+
 /* Synchronises `stream`, returns and clears the device status word
  * (SVDQ_OK, SVDQ_EINVAL or SVDQ_ETIMEOUT), or SVDQ_ECUDA on a runtime error. */
 svdq_status svdq_check_status(svdq_stream_t stream);

@@ -21,6 +21,7 @@ svdquant   page-1 contract in float64 (exact mode)
 codes      the fp32 op order that integer codes are compared in bit-exactly
 nvfp4      e2m1 / e4m3 formats, block quantisation, the 128x4 scale layout
 prepared   the linear evaluated from prepared (stored) operands
+attention  norm, rotation, paged cache and attention of heads between two linears
 
 Parity pins live in tests/test_oracle_*.py. The NVFP4 global/block scale
 recipe (gs = 448*6/amax, sf = e4m3(amax_b/6*gs)) is not printed on any page:

@@ -7,6 +7,11 @@ libsvdq.so is missing or no GPU is present, the calls raise.
     w = svdq_prepare(W, scale, rank, fmt="int4")          # one-time split on the GPU
     y = svdq_linear(w, x, bias=None, out_dtype=torch.bfloat16)
     y = svdq_linear_chain([w1, w2], x)                     # consecutive layers, PDL-chained
+    y = svdq_linear_chain([w_qkv, step, w_out], x)         # with attention between them
+
+Between the qkv and the output projection (rank_bit_residual_b200/attention.py):
+svdq_qk_norm_rope, svdq_kv_append, svdq_attention_prompt, svdq_attention_decode, and
+AttentionStep, which runs them as one step of svdq_linear_chain.
 
 Formats: "int2" .. "int8" (per-tensor grid), "nvfp4" (ue4m3 scales per 16
 elements and an fp32 global scale), "mxfp4" (E8M0 scales per 32 elements).
@@ -48,6 +53,19 @@ class SvdqWeight(ctypes.Structure):
                 ("ld", c_vp), ("ld32", c_vp), ("lu", c_vp), ("scale", c_vp), ("codes4", c_vp)]
 
 
+class SvdqHeads(ctypes.Structure):
+    _fields_ = [("data", c_vp), ("token_ld", c_i64), ("head_ld", c_i64), ("heads", c_i32)]
+
+
+class SvdqRope(ctypes.Structure):
+    _fields_ = [("turns", c_vp), ("rot_dim", c_i32), ("interleaved", c_i32), ("amplitude", ctypes.c_float)]
+
+
+class SvdqKvCache(ctypes.Structure):
+    _fields_ = [("k", c_vp), ("v", c_vp), ("pages", c_i64), ("page_ld", c_i64), ("slot_ld", c_i64),
+                ("head_ld", c_i64), ("page_size", c_i32), ("heads", c_i32), ("head_dim", c_i32)]
+
+
 _SIGS = {
     "svdq_version": (ctypes.c_char_p, []),
     "svdq_smooth_scale": (c_i32, [c_vp, c_i32, c_i64, c_i64, c_i64, c_vp, c_i32, c_i64, c_i64, ctypes.c_float,
@@ -77,6 +95,15 @@ _SIGS = {
     "svdq_quantize_act_noalloc": (c_i32, [c_vp, c_i32, c_i64, c_i64, c_i64, c_vp, SvdqFmt, c_vp, c_vp,
                                           c_vp, c_i32, c_vp, c_vp, c_vp, c_vp, c_vp]),
     "svdq_pack_int4": (c_i32, [c_vp, c_i64, c_i64, c_vp, c_vp]),
+    "svdq_qk_norm_rope": (c_i32, [SvdqHeads, SvdqHeads, c_i32, c_i64, c_i32, c_vp, SvdqRope, c_vp, c_vp, c_i32,
+                                  ctypes.c_float, SvdqHeads, SvdqHeads, c_vp]),
+    "svdq_kv_append": (c_i32, [ctypes.POINTER(SvdqKvCache), SvdqHeads, SvdqHeads, c_vp, c_i64, c_vp, SvdqRope, c_vp,
+                               c_i32, ctypes.c_float, SvdqHeads, c_vp, SvdqHeads, SvdqHeads, c_vp]),
+    "svdq_attention_prompt": (c_i32, [SvdqHeads, SvdqHeads, SvdqHeads, c_vp, c_vp, c_i32, c_i64, c_i64, c_i32, c_i32,
+                                      ctypes.c_float, SvdqHeads, c_vp]),
+    "svdq_attention_decode": (c_i32, [SvdqHeads, ctypes.POINTER(SvdqKvCache), c_vp, c_i64, c_vp, c_i32,
+                                      ctypes.c_float, SvdqHeads, c_vp, c_sz, c_vp]),
+    "svdq_attention_decode_workspace_size": (c_i32, [c_i32, c_i32, c_i32, c_i32, ctypes.POINTER(c_sz)]),
     "svdq_check_status": (c_i32, [c_vp]),
     "svdq_selftest_wait_timeout": (c_i32, [c_i64, c_vp]),
 }
@@ -462,11 +489,20 @@ def svdq_linear_chain(weights, x: torch.Tensor, biases=None, out_dtype=torch.bfl
     """Consecutive linears y_i = linear(w_i, y_{i-1}) (y_0 = x) on the current stream,
     every call after the first chained to the one before with PDL (pdl=True). Each
     intermediate y is in out_dtype (bf16 by default); ``outs`` may hold
-    preallocated outputs, one per linear."""
+    preallocated outputs, one per linear.
+
+    An entry of ``weights`` that is not a prepared weight is a step between two
+    linears, called with the y before it and returning the x of the next (e.g. an
+    AttentionStep); its entries in ``biases`` and ``outs`` must be None."""
     biases = biases if biases is not None else [None] * len(weights)
     ws = workspace or LinearWorkspace()
     y = x
     for i, (w, b) in enumerate(zip(weights, biases)):
+        if not isinstance(w, PreparedWeight):
+            if b is not None or (outs is not None and outs[i] is not None):
+                raise ValueError("a step between linears takes no bias and no preallocated output")
+            y = w(y)
+            continue
         y = svdq_linear(w, y, bias=b, out_dtype=out_dtype, workspace=ws, pdl=pdl and i > 0,
                         out=outs[i] if outs is not None else None)
     return y
@@ -547,11 +583,15 @@ def svdq_selftest_wait_timeout(limit_us: int = 1000) -> int:
     return load_library().svdq_selftest_wait_timeout(limit_us, _stream())
 
 
+from .attention import (AttentionStep, Rope, svdq_attention_decode, svdq_attention_prompt,  # noqa: E402
+                        svdq_kv_append, svdq_qk_norm_rope)
+
 __all__ = [
     "svdq_prepare", "svdq_quantize_act", "svdq_quantize_act_into", "svdq_quantize_act_noalloc",
     "svdq_quantize_residual", "svdq_linear", "svdq_linear_chain", "svdq_pack_int4", "svdq_fold_scale",
     "svdq_residual_product_i32", "svdq_residual_linear", "svdq_check_status", "svdq_selftest_wait_timeout",
-    "svdq_smooth_scale",
+    "svdq_smooth_scale", "svdq_qk_norm_rope", "svdq_kv_append", "svdq_attention_prompt", "svdq_attention_decode",
+    "AttentionStep", "Rope",
     "PreparedWeight", "LinearWorkspace", "allocate_weight", "weight_from_buffers",
     "weight_buffer_sizes", "load_library", "header_functions", "parse_fmt",
 ]

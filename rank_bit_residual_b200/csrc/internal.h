@@ -130,6 +130,36 @@ cudaError_t launch_gemm_fp4(const svdq_weight* w, const uint8_t* act_codes,
                             int64_t ldy, bool pdl, cudaStream_t stream, bool* bad_args,
                             void* split_ws = nullptr);
 
+// -------------------------------------------------- attention between linears
+// Norm and rotation of query and key heads (head_norm.cu). With a cache, rows of k
+// and v go to their slots too.
+struct HeadsArgs {
+  svdq_heads q, k, v, q_out, k_out;
+  svdq_kv_cache cache;       // cache.k = nullptr: none
+  const int64_t* slots;
+  const int64_t* positions;
+  svdq_rope rope;
+  const void* q_weight;
+  const void* k_weight;
+  bool weight_bf16;
+  float eps;
+  int64_t tokens;
+  int head_dim;
+  unsigned* status;
+};
+cudaError_t launch_heads(const HeadsArgs& a, svdq_dtype dtype, cudaStream_t stream);
+
+// Attention over packed prompts (prompt_attention.cu).
+cudaError_t launch_prompt(const svdq_heads& q, const svdq_heads& k, const svdq_heads& v, const int32_t* cu_q,
+                          const int32_t* cu_k, int batch, int64_t q_tokens, int64_t k_tokens, int head_dim,
+                          bool causal, float scale, const svdq_heads& out, cudaStream_t stream, bool* bad_args);
+
+// Attention of one token per sequence over a paged cache (paged_attention.cu).
+size_t paged_scratch_bytes(int heads, int kv_heads, int head_dim);
+cudaError_t launch_paged(const svdq_heads& q, const svdq_kv_cache& cache, const int32_t* page_table,
+                         int64_t table_ld, const int32_t* kv_len, int batch, float scale, const svdq_heads& out,
+                         void* scratch, cudaStream_t stream);
+
 // -------------------------------------------------------------- quantisers
 size_t residual_scratch_bytes(int64_t M, int64_t N);
 cudaError_t launch_quantize_residual(const float* R, int64_t M, int64_t N, int64_t ldR,
