@@ -2,10 +2,30 @@
 //
 //   out = sum_j p_j v_j / sum_j p_j,   p_j = exp(scale q . k_j - m),   m = the running maximum
 //
-// A block takes 64 rows of one head; four warps of 16 rows walk over the keys in
-// tiles of 64 with a running maximum and sum, products on the warp tensor instructions.
+// One pass over the keys with a running maximum and sum. A block works on an item of two
+// tiles of 128 query rows that share their keys: the same rows of two query heads of one
+// key head when the group is even, else 256 consecutive rows of one head. Per tile of 128
+// keys and 128 rows, S = Q K^T goes to tensor memory, four warps (one row per
+// thread, so row maxima and sums need no exchange) turn it into P = 2^(S c - m) in bf16
+// and put it back over S, and O += P V accumulates in tensor memory with P as the operand
+// from there. While one tile's S is in softmax, the tensor cores work on the other's
+// products: with 128-element heads a tile costs 1024 cycles of products and 1024 of
+// exponentials (16 a cycle), so both bound the kernel.
+//
+// The maximum is renewed (and O rescaled, by the softmax warps themselves) only when a
+// score passes it by 2^8; P then stays below 2^8, and both sums are fp32. Because
+// products run in order, S(j) complete means that O holds all tiles before j: no further
+// barrier guards the rescaling.
+//
+// Warps: 0-3 and 4-7 softmax and output of the two tiles, 8 the products, 9 the loads and the
+// choice of items (blocks that have not started are taken over, so that long and short
+// items balance), 10 cleans values: in tiles that hold a key some row does not see,
+// rows behind the sequence's end become zero, and infinities and NaN too (a zero weight
+// must not meet them); the latter are added at the end to the rows that do see them.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
+
+#include <algorithm>
 
 #include "internal.h"
 #include "ptx.cuh"
@@ -14,9 +34,11 @@ namespace svdq {
 
 namespace {
 
-constexpr int kThreads = 128;
-constexpr int kRows = 64;   // query rows of a block
-constexpr int kKeys = 64;   // keys of a tile
+constexpr int kRows = 128;      // query rows of a tile
+constexpr int kKeys = 128;      // keys of a tile
+constexpr int kThreads = 384;
+constexpr int kItems = 4;       // items between the chooser and the slowest reader
+constexpr int kSoftmaxRegs = 216, kOtherRegs = 72;   // 256 * 216 + 128 * 72 = 384 * 168
 
 struct PromptArgs {
   svdq_heads q, k, v, out;
@@ -25,8 +47,22 @@ struct PromptArgs {
   int batch;
   int64_t q_tokens, k_tokens;
   int dim, causal;
+  int tile_rows;    // rows of a sequence that an item covers: 128 (two heads) or 256
+  int pairs;        // items per row range: heads / 2 or heads
   float scale_log2;
   unsigned* status;
+};
+
+struct Item {
+  int valid;        // 0: no more
+  int keys, k0;     // keys of the sequence and their first row
+  int kvh;
+  int n[2];         // key tiles of each row tile
+  int cut;          // first key tile with a key that some row does not see
+  int row[2];       // first row in q and out
+  int rows[2];      // rows inside the sequence, 0 .. 128
+  int head[2];
+  int seen[2];      // keys that the tile's first row sees (causal; row r sees r more)
 };
 
 // Start of sequence s (no list: one sequence of all rows).
@@ -39,28 +75,23 @@ __device__ __forceinline__ bool bad_cu(const int32_t* cu, int s, long long token
   return cu && (cu[s] < 0 || cu[s + 1] < cu[s] || cu[s + 1] > tokens);
 }
 
-struct Tile {
-  int seq;        // -1: past the last tile
-  int row0;       // first row of the tile in its sequence
-  long long q0;   // first row of the sequence in q
-  int rows;       // rows of the sequence
-  long long k0;
-  int keys;
-};
-
-// The tile `index` of the line of all sequences' row tiles; every thread of the block calls it.
-__device__ Tile find_tile(const PromptArgs& a, long long index) {
-  __shared__ int sh_warp[kThreads / 32];
-  __shared__ Tile sh_tile;
-  if (threadIdx.x == 0) sh_tile.seq = -1;
-  long long before = 0;
-  for (int s0 = 0; s0 < a.batch; s0 += kThreads) {
-    const int s = s0 + threadIdx.x;
-    int n = 0;
-    long long q0 = 0, q1 = 0;
+// Item `index` of the line: row ranges of all sequences, each with its `pairs` heads. The
+// whole warp calls it; valid = 0 past the last range.
+__device__ Item find_item(const PromptArgs& a, int index) {
+  const int lane = threadIdx.x & 31;
+  const int range = index / a.pairs, pair = index - range * a.pairs;
+  Item it;
+  it.valid = 0;
+  int before = 0;
+  for (int s0 = 0; s0 < a.batch; s0 += 32) {
+    const int s = s0 + lane;
+    int n = 0, q0 = 0, rows = 0, k0 = 0, keys = 0;
     if (s < a.batch) {
-      q0 = cu_at(a.cu_q, s, a.q_tokens), q1 = cu_at(a.cu_q, s + 1, a.q_tokens);
-      n = static_cast<int>(max(0ll, q1 - q0 + kRows - 1) / kRows);
+      q0 = static_cast<int>(cu_at(a.cu_q, s, a.q_tokens));
+      rows = max(0, static_cast<int>(cu_at(a.cu_q, s + 1, a.q_tokens)) - q0);
+      k0 = static_cast<int>(cu_at(a.cu_k, s, a.k_tokens));
+      keys = max(0, static_cast<int>(cu_at(a.cu_k, s + 1, a.k_tokens)) - k0);
+      n = (rows + a.tile_rows - 1) / a.tile_rows;
       if (index == 0 && (bad_cu(a.cu_q, s, a.q_tokens) || bad_cu(a.cu_k, s, a.k_tokens)))
         record_status(a.status, kStatusEinval);
     }
@@ -68,53 +99,53 @@ __device__ Tile find_tile(const PromptArgs& a, long long index) {
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int up = __shfl_up_sync(0xffffffffu, incl, o);
-      if ((threadIdx.x & 31) >= o) incl += up;
+      if (lane >= o) incl += up;
     }
-    __syncthreads();
-    if ((threadIdx.x & 31) == 31) sh_warp[threadIdx.x >> 5] = incl;
-    __syncthreads();
-    int chunk = 0;
+    const unsigned hit = __ballot_sync(0xffffffffu, before + incl > range);
+    if (hit != 0) {
+      const int src = __ffs(hit) - 1;
+      const int first = before + __shfl_sync(0xffffffffu, incl - n, src);
+      n = __shfl_sync(0xffffffffu, n, src);
+      q0 = __shfl_sync(0xffffffffu, q0, src);
+      rows = __shfl_sync(0xffffffffu, rows, src);
+      k0 = __shfl_sync(0xffffffffu, k0, src);
+      keys = __shfl_sync(0xffffffffu, keys, src);
+      // the last ranges of a causal sequence see the most keys: they go first
+      const int r0 = (n - 1 - (range - first)) * a.tile_rows;
+      it.valid = 1;
+      it.keys = keys, it.k0 = k0;
+      const bool two_heads = a.tile_rows == kRows;
+      it.cut = 0x7FFFFFFF;
 #pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) {
-      if (w < (threadIdx.x >> 5)) incl += sh_warp[w];
-      chunk += sh_warp[w];
+      for (int t = 0; t < 2; ++t) {
+        const int row = two_heads ? r0 : r0 + t * kRows;
+        it.head[t] = two_heads ? 2 * pair + t : pair;
+        it.row[t] = q0 + row;
+        it.rows[t] = max(0, min(kRows, rows - row));
+        it.seen[t] = a.causal ? keys - rows + row + 1 : keys;
+        const int last = a.causal ? min(keys, it.seen[t] + it.rows[t] - 1) : keys;
+        it.n[t] = it.rows[t] > 0 ? max(0, last + kKeys - 1) / kKeys : 0;
+        it.cut = min(it.cut, max(0, min(keys, it.seen[t])) / kKeys);
+      }
+      it.kvh = it.head[0] / (a.q.heads / a.k.heads);
+      return it;
     }
-    if (before + incl - n <= index && index < before + incl) {
-      sh_tile.seq = s;
-      sh_tile.row0 = static_cast<int>(index - (before + incl - n)) * kRows;
-      sh_tile.q0 = q0;
-      sh_tile.rows = static_cast<int>(q1 - q0);
-      sh_tile.k0 = cu_at(a.cu_k, s, a.k_tokens);
-      sh_tile.keys = static_cast<int>(max(0ll, cu_at(a.cu_k, s + 1, a.k_tokens) - sh_tile.k0));
-    }
-    before += chunk;
-    if (before > index) break;
+    before += __shfl_sync(0xffffffffu, incl, 31);
   }
-  __syncthreads();
-  return sh_tile;
-}
-
-__device__ __forceinline__ void ldmatrix_x4(uint32_t saddr, uint32_t (&r)[4]) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(saddr)
-               : "memory");
-}
-__device__ __forceinline__ void ldmatrix_x4_trans(uint32_t saddr, uint32_t (&r)[4]) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(saddr)
-               : "memory");
+  return it;
 }
 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&v);
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
 }
 
-// exp2 of a difference to a maximum; a score of -inf counts nothing, even while the
-// maximum is -inf itself (no key yet).
-__device__ __forceinline__ float exp2_from(float x, float top) { return x == -INFINITY ? 0.0f : exp2f(x - top); }
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
 
 // The bf16 pairs of a word, infinities and NaN replaced by zero; sets *found then.
 __device__ __forceinline__ uint32_t finite_or_zero(uint32_t w, bool* found) {
@@ -123,143 +154,450 @@ __device__ __forceinline__ uint32_t finite_or_zero(uint32_t w, bool* found) {
   return w;
 }
 
+template <int kRegs>
+__device__ __forceinline__ void regs_up() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+template <int kRegs>
+__device__ __forceinline__ void regs_down() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+
 template <int kDim>
-__global__ void __launch_bounds__(kThreads) prompt_kernel(const PromptArgs a) {
-  __shared__ __align__(128) unsigned char sh_k[kKeys * kDim * 2], sh_v[kKeys * kDim * 2];
-  __shared__ int sh_odd;   // a value that is not finite behind some row's place
-  if (threadIdx.x == 0) sh_odd = 0;
-  const Tile t = find_tile(a, blockIdx.x);
-  if (t.seq < 0) return;
+struct Shape {
+  static constexpr int kTile = kKeys * kDim * 2;         // bytes of 128 rows of a head
+  static constexpr int kRing = kDim == 128 ? 5 : 10;     // tiles of keys and values in flight
+  static constexpr int kSmem = 2 * kTile + kRing * kTile + 1024;
+  static constexpr int kO = 256;                         // tensor memory columns: S0, S1, O0, O1
+};
+
+template <int kRing>
+struct Barriers {
+  uint64_t q_full, q_empty;
+  uint64_t full[kRing], empty[kRing];
+  uint64_t raw[kRing];   // loaded, for the cleaning warp, which then completes `full`
+  uint64_t s_full[2], p_full[2], o_full[2];
+  uint64_t item_full[kItems], item_empty[kItems];
+  uint64_t answer;
+};
+
+// A ring position and its phase.
+template <int kN>
+struct Turn {
+  int i = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ void next() {
+    if (++i == kN) i = 0, phase ^= 1;
+  }
+};
+
+template <int kDim>
+__global__ void __launch_bounds__(kThreads, 1)
+    prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
+                  const __grid_constant__ CUtensorMap map_v, const __grid_constant__ PromptArgs a) {
+  using Sz = Shape<kDim>;
+  extern __shared__ unsigned char smem_raw[];
+  __shared__ Barriers<Sz::kRing> bar;
+  __shared__ Item items[kItems];
+  __shared__ int odd[2 * kItems];        // by item number (from 1): the number, if values were taken out
+  __shared__ uint32_t tmem_base;
+  __shared__ int abort_flag;
+  __shared__ __align__(16) uint4 answer;
+
+  unsigned char* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+  unsigned char* sq = smem;              // two tiles of Q
+  unsigned char* ring = smem + 2 * Sz::kTile;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int h = blockIdx.y, kvh = h / (a.q.heads / a.k.heads);
-  const int r0 = t.row0 + warp * 16 + (lane >> 2);   // this lane's rows: r0 and r0 + 8
+  volatile int* abort = &abort_flag;
 
-  const __nv_bfloat16* qp = static_cast<const __nv_bfloat16*>(a.q.data) + t.q0 * a.q.token_ld + h * a.q.head_ld;
-  const __nv_bfloat16* kp = static_cast<const __nv_bfloat16*>(a.k.data) + t.k0 * a.k.token_ld + kvh * a.k.head_ld;
-  const __nv_bfloat16* vp = static_cast<const __nv_bfloat16*>(a.v.data) + t.k0 * a.v.token_ld + kvh * a.v.head_ld;
+  if (threadIdx.x == 0) {
+    abort_flag = 0;
+    mbar_init(&bar.q_full, 1);
+    mbar_init(&bar.q_empty, 1);
+    for (int i = 0; i < Sz::kRing; ++i) {
+      mbar_init(&bar.full[i], 1);
+      mbar_init(&bar.empty[i], 1);
+      mbar_init(&bar.raw[i], 1);
+    }
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(&bar.s_full[t], 1);
+      mbar_init(&bar.p_full[t], 4);
+      mbar_init(&bar.o_full[t], 1);
+    }
+    for (int i = 0; i < kItems; ++i) {
+      mbar_init(&bar.item_full[i], 1);
+      mbar_init(&bar.item_empty[i], 10);   // 8 softmax warps, the products, the cleaning warp
+      odd[i] = odd[kItems + i] = 0;
+    }
+    mbar_init(&bar.answer, 1);
+    fence_mbar_init();
+    tma_prefetch_desc(&map_q);
+    tma_prefetch_desc(&map_k);
+    tma_prefetch_desc(&map_v);
+  }
+  if (warp == 8) {
+    tmem_alloc(&tmem_base, 512);
+    tmem_relinquish();
+  }
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_base;
 
-  uint32_t qf[kDim / 16][4];
-#pragma unroll
-  for (int kk = 0; kk < kDim / 16; ++kk)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int row = r0 + (i & 1) * 8, e = kk * 16 + (i >> 1) * 8 + 2 * (lane & 3);
-      qf[kk][i] = row < t.rows && e < a.dim ? *reinterpret_cast<const uint32_t*>(qp + row * a.q.token_ld + e) : 0u;
-    }
-  float o[kDim / 8][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
-#pragma unroll
-  for (int i = 0; i < kDim / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.0f;
-
-  const int shift = t.keys - t.rows;   // row r sees keys 0 .. shift + r
-  const int last = a.causal ? min(t.keys, min(t.rows, t.row0 + kRows) + shift) : t.keys;
-  // Tiles from here on hold keys that some row does not see. A value there that is not
-  // finite must not meet that row's zero weight (0 * NaN): it is taken out of the product
-  // and added at the end to the rows that see it.
-  const int cut = a.causal ? max(0, t.row0 + shift + 1) / kKeys * kKeys : last;
-  for (int key0 = 0; key0 < last; key0 += kKeys) {
-    __syncthreads();
-    for (int i = threadIdx.x; i < kKeys * (kDim / 8); i += kThreads) {
-      const int row = i / (kDim / 8), c = i % (kDim / 8);
-      const bool on = key0 + row < t.keys && c * 8 < a.dim;
-      const int at = row * kDim * 2 + ((c ^ (row & 7)) << 4);
-      cp_async16(sh_k + at, on ? kp + (key0 + row) * a.k.token_ld + c * 8 : kp, on ? 16 : 0);
-      cp_async16(sh_v + at, on ? vp + (key0 + row) * a.v.token_ld + c * 8 : vp, on ? 16 : 0);
-    }
-    cp_async_commit();
-    cp_async_wait<0>();
-    if (key0 >= cut) {
-      bool found = false;
-      for (int i = threadIdx.x; i < kKeys * (kDim / 8); i += kThreads) {   // what this thread has copied
-        const int row = i / (kDim / 8), c = i % (kDim / 8);
-        uint4* w = reinterpret_cast<uint4*>(sh_v + row * kDim * 2 + ((c ^ (row & 7)) << 4));
-        uint4 x = *w;
-        x.x = finite_or_zero(x.x, &found), x.y = finite_or_zero(x.y, &found);
-        x.z = finite_or_zero(x.z, &found), x.w = finite_or_zero(x.w, &found);
-        *w = x;
-      }
-      if (found) sh_odd = 1;
-    }
-    __syncthreads();
-
-    float s[kKeys / 8][4];
-#pragma unroll
-    for (int n = 0; n < kKeys / 8; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.0f;
-#pragma unroll
-    for (int n = 0; n < kKeys / 16; ++n)
-#pragma unroll
-      for (int kk = 0; kk < kDim / 16; ++kk) {
-        uint32_t f[4];
-        const int row = n * 16 + (lane & 7) + (lane >> 4) * 8, c = 2 * kk + ((lane >> 3) & 1);
-        ldmatrix_x4(smem_u32(sh_k) + row * kDim * 2 + ((c ^ (row & 7)) << 4), f);
-        const uint32_t b0[2] = {f[0], f[1]}, b1[2] = {f[2], f[3]};
-        mma_bf16_16816(s[2 * n], qf[kk], b0);
-        mma_bf16_16816(s[2 * n + 1], qf[kk], b1);
-      }
-    float top[2] = {m[0], m[1]};
-#pragma unroll
-    for (int n = 0; n < kKeys / 8; ++n)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int key = key0 + n * 8 + 2 * (lane & 3) + (i & 1), row = r0 + (i >> 1) * 8;
-        const bool on = key < t.keys && (!a.causal || key <= row + shift);
-        s[n][i] = on ? s[n][i] * a.scale_log2 : -INFINITY;
-        top[i >> 1] = fmaxf(top[i >> 1], s[n][i]);
-      }
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], 1));
-      top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], 2));
-      const float f = exp2_from(m[i], top[i]);
-      m[i] = top[i];
-      l[i] *= f;
-#pragma unroll
-      for (int d = 0; d < kDim / 8; ++d) o[d][2 * i] *= f, o[d][2 * i + 1] *= f;
-    }
-#pragma unroll
-    for (int n = 0; n < kKeys / 16; ++n) {
-#pragma unroll
-      for (int j = 2 * n; j < 2 * n + 2; ++j)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          s[j][i] = exp2_from(s[j][i], m[i >> 1]);
-          l[i >> 1] += s[j][i];
+  if (warp >= 8) {
+    regs_down<kOtherRegs>();
+    if (warp == 9) {
+      // ---------------------------------------------------------- items and loads
+      Turn<kItems> slot;
+      Turn<Sz::kRing> r;
+      uint32_t q_phase = 0, answer_phase = 0, last_raw = 0, raw_phase = 0;   // the last two by ring position
+      int index = blockIdx.x;
+      bool ok = true;
+      while (ok) {
+        // ask for the next item while this one is worked on
+        if (lane == 0 && index >= 0) {
+          mbar_arrive_expect_tx(&bar.answer, 16);
+          block_request(&answer, &bar.answer);
         }
-      const uint32_t pf[4] = {pack_bf16(s[2 * n][0], s[2 * n][1]), pack_bf16(s[2 * n][2], s[2 * n][3]),
-                              pack_bf16(s[2 * n + 1][0], s[2 * n + 1][1]), pack_bf16(s[2 * n + 1][2], s[2 * n + 1][3])};
+        Item it;
+        it.valid = 0;
+        if (index >= 0) it = find_item(a, index);
+        if (index < 0 || it.valid) {
+          ok = mbar_wait_warp(&bar.item_empty[slot.i], slot.phase ^ 1, a.status, abort);
+          if (ok && lane == 0) {
+            items[slot.i] = it;
+            mbar_arrive(&bar.item_full[slot.i]);
+          }
+          slot.next();
+        }
+        if (index < 0) break;
+        const int n = it.valid ? max(it.n[0], it.n[1]) : 0;
+        if (ok && n > 0 && lane == 0) {
+          ok = mbar_wait(&bar.q_empty, q_phase ^ 1, a.status, abort);
+          q_phase ^= 1;
+          if (ok) {
+            mbar_arrive_expect_tx(&bar.q_full, 2 * Sz::kTile);
 #pragma unroll
-      for (int d = 0; d < kDim / 16; ++d) {
-        uint32_t f[4];
-        const int row = n * 16 + (lane & 15), c = 2 * d + (lane >> 4);
-        ldmatrix_x4_trans(smem_u32(sh_v) + row * kDim * 2 + ((c ^ (row & 7)) << 4), f);
-        const uint32_t b0[2] = {f[0], f[1]}, b1[2] = {f[2], f[3]};
-        mma_bf16_16816(o[2 * d], pf, b0);
-        mma_bf16_16816(o[2 * d + 1], pf, b1);
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+              for (int c = 0; c < kDim / 64; ++c)
+                tma_load_3d(sq + t * Sz::kTile + c * kRows * 128, &map_q, &bar.q_full, c * 64, it.head[t], it.row[t]);
+          }
+          for (int j = 0; ok && j < 2 * n; ++j) {   // K0, V0, K1, V1, ...
+            ok = mbar_wait(&bar.empty[r.i], r.phase ^ 1, a.status, abort);
+            if (!ok) break;
+            const bool raw = (j & 1) && (j >> 1) >= it.cut;
+            uint64_t* to = raw ? &bar.raw[r.i] : &bar.full[r.i];
+            last_raw = (last_raw & ~(1u << r.i)) | (raw ? 1u << r.i : 0u);
+            if (raw) raw_phase ^= 1u << r.i;
+            mbar_arrive_expect_tx(to, Sz::kTile);
+#pragma unroll
+            for (int c = 0; c < kDim / 64; ++c)
+              tma_load_3d(ring + r.i * Sz::kTile + c * kKeys * 128, (j & 1) ? &map_v : &map_k, to, c * 64, it.kvh,
+                          it.k0 + (j >> 1) * kKeys);
+            r.next();
+          }
+        }
+        ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+        int got = -1;
+        if (lane == 0) {
+          // also on an abort: the answer must have landed before the block ends
+          if (mbar_wait(&bar.answer, answer_phase, a.status, nullptr)) got = block_answer(&answer);
+          fence_proxy_async_smem();
+        }
+        answer_phase ^= 1;
+        index = __shfl_sync(0xffffffffu, got, 0);
+      }
+      // nothing may still be in flight when the block ends
+      if (lane == 0 && *abort) {
+        mbar_wait(&bar.q_full, q_phase ^ 1, a.status, nullptr);
+        Turn<Sz::kRing> w = r;
+        for (int i = 0; i < Sz::kRing; ++i) {
+          if ((last_raw >> w.i) & 1)
+            mbar_wait(&bar.raw[w.i], ((raw_phase >> w.i) & 1) ^ 1, a.status, nullptr);
+          else
+            mbar_wait(&bar.full[w.i], w.phase ^ 1, a.status, nullptr);
+          w.next();
+        }
+      }
+    } else if (warp == 8) {
+      // ------------------------------------------------------------------ products
+      if (lane == 0) {
+        constexpr uint32_t idesc_s = idesc_bf16(kRows, kKeys), idesc_o = idesc_bf16_bmn(kRows, kDim);
+        Turn<kItems> slot;
+        Turn<Sz::kRing> r;
+        uint32_t q_phase = 0, p_phase[2] = {0, 0};
+        bool ok = true;
+        auto scores = [&](int t, int buf) {
+          const uint32_t qa = smem_u32(sq + t * Sz::kTile), kb = smem_u32(ring + buf * Sz::kTile);
+#pragma unroll
+          for (int kk = 0; kk < kDim / 16; ++kk) {
+            const uint32_t off = (kk >> 2) * (kRows * 128) + (kk & 3) * 32;
+            mma_f16(tmem + t * kKeys, smem_desc_sw128(qa + off), smem_desc_sw128(kb + off), idesc_s, kk > 0);
+          }
+          mma_commit(&bar.s_full[t]);
+        };
+        while (true) {
+          ok = mbar_wait(&bar.item_full[slot.i], slot.phase, a.status, abort);
+          if (!ok) break;
+          const Item it = items[slot.i];
+          mbar_arrive(&bar.item_empty[slot.i]);
+          slot.next();
+          if (!it.valid) break;
+          const int n = max(it.n[0], it.n[1]);
+          if (n == 0) continue;
+          ok = mbar_wait(&bar.q_full, q_phase, a.status, abort) && mbar_wait(&bar.full[r.i], r.phase, a.status, abort);
+          q_phase ^= 1;
+          if (!ok) break;
+          tc_fence_after();
+#pragma unroll
+          for (int t = 0; t < 2; ++t)
+            if (it.n[t] > 0) scores(t, r.i);
+          mma_commit(&bar.empty[r.i]);
+          if (n == 1) mma_commit(&bar.q_empty);
+          r.next();
+          for (int j = 0; ok && j < n; ++j) {
+            const int vbuf = r.i;
+            ok = mbar_wait(&bar.full[vbuf], r.phase, a.status, abort);
+            r.next();
+            const bool more = j + 1 < n;
+            const int kbuf = r.i;
+            bool have_k = false;
+            const uint32_t vb = smem_u32(ring + vbuf * Sz::kTile);
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+              if (ok && j < it.n[t]) {
+                ok = mbar_wait(&bar.p_full[t], p_phase[t], a.status, abort);
+                p_phase[t] ^= 1;
+                if (ok) {
+                  tc_fence_after();
+#pragma unroll
+                  for (int kk = 0; kk < kKeys / 16; ++kk)
+                    mma_f16_ta(tmem + Sz::kO + t * kDim, tmem + t * kKeys + kk * 8,
+                               smem_desc_sw128_mn(vb + kk * 2048, kKeys * 128), idesc_o, j > 0 || kk > 0);
+                  if (j == it.n[t] - 1) mma_commit(&bar.o_full[t]);
+                }
+              }
+              if (ok && j + 1 < it.n[t]) {
+                if (!have_k) {
+                  ok = mbar_wait(&bar.full[kbuf], r.phase, a.status, abort);
+                  have_k = true;
+                  tc_fence_after();
+                }
+                if (ok) scores(t, kbuf);
+              }
+            }
+            if (!ok) break;
+            mma_commit(&bar.empty[vbuf]);
+            if (more) {
+              mma_commit(&bar.empty[kbuf]);
+              if (j + 2 == n) mma_commit(&bar.q_empty);
+              r.next();
+            }
+          }
+          if (!ok) break;
+        }
+      }
+    } else if (warp == 10) {
+      // ----------------------------------------------------------------- cleaning
+      Turn<kItems> slot;
+      Turn<Sz::kRing> r;
+      int number = 0;
+      uint32_t raw_phase = 0;              // by ring position
+      while (true) {
+        if (!mbar_wait_warp(&bar.item_full[slot.i], slot.phase, a.status, abort)) break;
+        const Item it = items[slot.i];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar.item_empty[slot.i]);
+        slot.next();
+        if (!it.valid) break;
+        ++number;
+        const int n = max(it.n[0], it.n[1]);
+        bool ok = true;
+        for (int j = 0; ok && j < n; ++j) {
+          r.next();                        // the keys
+          if (j >= it.cut) {
+            ok = mbar_wait_warp(&bar.raw[r.i], (raw_phase >> r.i) & 1, a.status, abort);
+            if (!ok) break;
+            raw_phase ^= 1u << r.i;
+            bool found = false;
+            const int inside = it.keys - j * kKeys;
+            unsigned char* base = ring + r.i * Sz::kTile;
+            // 16-byte pieces in memory order: 8 to a row of 64 elements, whatever the swizzle
+            for (int i = lane; i < Sz::kTile / 16; i += 32) {
+              uint4* w = reinterpret_cast<uint4*>(base + i * 16);
+              if ((i >> 3) % kKeys >= inside) {
+                *w = make_uint4(0, 0, 0, 0);
+              } else {
+                const uint4 x = *w;
+                bool here = false;
+                const uint4 y = make_uint4(finite_or_zero(x.x, &here), finite_or_zero(x.y, &here),
+                                           finite_or_zero(x.z, &here), finite_or_zero(x.w, &here));
+                if (here) *w = y, found = true;
+              }
+            }
+            if (found) odd[number % (2 * kItems)] = number;
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar.full[r.i]);
+          }
+          r.next();
+        }
+        if (!ok) break;
       }
     }
-  }
+  } else {
+    // ------------------------------------------------------------ softmax and output
+    regs_up<kSoftmaxRegs>();
+    const int t = warp >> 2;
+    const int row = (warp & 3) * 32 + lane;   // of the tile
+    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t ts = tmem + lanes + t * kKeys, to = tmem + lanes + Sz::kO + t * kDim;
+    // The scores take the sign. A scale of zero is one so small that all weights are 1, and
+    // a masked -inf still comes out as a weight of 0.
+    const float scale = fmaxf(fabsf(a.scale_log2), 1e-30f);
+    Turn<kItems> slot;
+    uint32_t s_phase = 0, o_phase = 0;
+    int number = 0;
+    while (true) {
+      if (!mbar_wait_warp(&bar.item_full[slot.i], slot.phase, a.status, abort)) break;
+      const Item& sh = items[slot.i];
+      const int valid = sh.valid, keys = sh.keys, k0 = sh.k0, kvh = sh.kvh, n = sh.n[t], cut = sh.cut;
+      const int row0 = sh.row[t], rows = sh.rows[t], head = sh.head[t];
+      const int seen = a.causal ? min(keys, sh.seen[t] + row) : keys;   // keys of this row
+      const int all_see = min(keys, sh.seen[t]);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar.item_empty[slot.i]);
+      slot.next();
+      if (!valid) break;
+      ++number;
+      float m = -INFINITY, l = 0.0f;
+      bool ok = true;
+      for (int j = 0; j < n; ++j) {
+        ok = mbar_wait(&bar.s_full[t], s_phase, a.status, abort);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        s_phase ^= 1;
+        tc_fence_after();
+        uint32_t s[kKeys / 32][32];
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
-    l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
-    const int row = r0 + 8 * i;
-    if (row >= t.rows) continue;
-    const float inv = l[i] == 0.0f ? 0.0f : 1.0f / l[i];
-    if (sh_odd) {
-      for (int j = cut; j <= row + shift && j < t.keys; ++j)
+        for (int c = 0; c < kKeys / 32; ++c) tmem_ld_32x32b_x32(ts + c * 32, s[c]);
+        tmem_ld_wait();
 #pragma unroll
-        for (int d = 0; d < kDim / 8; ++d)
-          for (int b = 0; b < 2; ++b) {
-            const int e = d * 8 + 2 * (lane & 3) + b;
-            const float x = e < a.dim ? __bfloat162float(vp[j * a.v.token_ld + e]) : 0.0f;
-            if (!isfinite(x)) o[d][2 * i + b] += x;
+        for (int c = 0; c < kKeys / 32; ++c)
+#pragma unroll
+          for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(s[c][i]));
+        if (a.scale_log2 < 0.0f) {
+#pragma unroll
+          for (int c = 0; c < kKeys / 32; ++c)
+#pragma unroll
+            for (int i = 0; i < 32; ++i) s[c][i] ^= 0x80000000u;
+        }
+        if ((j + 1) * kKeys > all_see) {
+          const int left = seen - j * kKeys;
+#pragma unroll
+          for (int c = 0; c < kKeys / 32; ++c)
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (c * 32 + i >= left) s[c][i] = 0xFF800000u;   // -inf
+        }
+        float top = -INFINITY;
+#pragma unroll
+        for (int c = 0; c < kKeys / 32; ++c)
+#pragma unroll
+          for (int i = 0; i < 32; ++i) top = fmaxf(top, __uint_as_float(s[c][i]));
+        top *= scale;
+        if (__any_sync(0xffffffffu, top > m + 8.0f || (m == -INFINITY && top > m))) {
+          const float up = fmaxf(m, top);
+          const float f = m == -INFINITY ? 0.0f : ex2(m - up);
+          m = up;
+          l *= f;
+          if (j > 0) {
+#pragma unroll
+            for (int c = 0; c < kDim / 32; ++c) {
+              uint32_t o[32];
+              tmem_ld_32x32b_x32(to + c * 32, o);
+              tmem_ld_wait_regs(o);
+#pragma unroll
+              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+              tmem_st_32x32b_x32(to + c * 32, o);
+            }
           }
-    }
-    __nv_bfloat16* dst =
-        static_cast<__nv_bfloat16*>(a.out.data) + (t.q0 + row) * a.out.token_ld + h * a.out.head_ld + 2 * (lane & 3);
+        }
+        const float base = m == -INFINITY ? 0.0f : -m;
 #pragma unroll
-    for (int d = 0; d < kDim / 8; ++d)
-      if (d * 8 < a.dim) *reinterpret_cast<uint32_t*>(dst + d * 8) = pack_bf16(o[d][2 * i] * inv, o[d][2 * i + 1] * inv);
+        for (int c = 0; c < kKeys / 32; ++c) {
+          uint32_t p[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const float x = ex2(fmaf(__uint_as_float(s[c][2 * i]), scale, base));
+            const float y = ex2(fmaf(__uint_as_float(s[c][2 * i + 1]), scale, base));
+            l += x + y;
+            p[i] = pack_bf16(x, y);
+          }
+          tmem_st_32x32b_x16(ts + c * 16, p);
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar.p_full[t]);
+      }
+      if (!ok) break;
+      if (n > 0) {
+        ok = mbar_wait(&bar.o_full[t], o_phase, a.status, abort);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        o_phase ^= 1;
+        tc_fence_after();
+      }
+      const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+      const bool extra = n > 0 && odd[number % (2 * kItems)] == number;
+      __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.out.data) +
+                           static_cast<long long>(row0 + row) * a.out.token_ld + head * a.out.head_ld;
+#pragma unroll
+      for (int c = 0; c < kDim / 32; ++c) {
+        uint32_t o[32];
+        if (n > 0) {
+          tmem_ld_32x32b_x32(to + c * 32, o);
+          tmem_ld_wait_regs(o);
+        }
+        if (extra && row < rows) {
+          const __nv_bfloat16* vp = static_cast<const __nv_bfloat16*>(a.v.data) + kvh * a.v.head_ld;
+          for (int key = cut * kKeys; key < seen; ++key)
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              const float x = c * 32 + i < a.dim ? __bfloat162float(vp[(k0 + key) * a.v.token_ld + c * 32 + i]) : 0.0f;
+              if (!isfinite(x)) o[i] = __float_as_uint(__uint_as_float(o[i]) + x);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 32; i += 8) {
+          uint32_t w[4];
+#pragma unroll
+          for (int b = 0; b < 4; ++b)
+            w[b] = n > 0 ? pack_bf16(__uint_as_float(o[i + 2 * b]) * inv, __uint_as_float(o[i + 2 * b + 1]) * inv) : 0u;
+          if (row < rows && c * 32 + i < a.dim)
+            *reinterpret_cast<uint4*>(dst + c * 32 + i) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+      }
+      tc_fence_before();
+    }
   }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 8) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+template <int kDim>
+cudaError_t launch_dim(const PromptArgs& a, const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv,
+                       unsigned grid, cudaStream_t st) {
+  constexpr int smem = Shape<kDim>::kSmem;
+  cudaError_t e = cudaFuncSetAttribute(prompt_kernel<kDim>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  prompt_kernel<kDim><<<grid, kThreads, smem, st>>>(mq, mk, mv, a);
+  return cudaGetLastError();
 }
 
 }  // namespace
@@ -267,15 +605,21 @@ __global__ void __launch_bounds__(kThreads) prompt_kernel(const PromptArgs a) {
 cudaError_t launch_prompt(const svdq_heads& q, const svdq_heads& k, const svdq_heads& v, const int32_t* cu_q,
                           const int32_t* cu_k, int batch, int64_t q_tokens, int64_t k_tokens, int head_dim,
                           bool causal, float scale, const svdq_heads& out, cudaStream_t stream, bool* bad_args) {
+  const int group = q.heads / k.heads;
+  // Two heads that share their keys make a better pair than two row ranges: both tiles see
+  // the same keys, and a sequence's last range wastes fewer rows.
+  const bool two_heads = group % 2 == 0;
   PromptArgs a{q, k, v, out, cu_q, cu_k, batch, q_tokens, k_tokens, head_dim, causal ? 1 : 0,
-               scale * 1.4426950408889634f, device_status_word()};
-  *bad_args = false;
-  const dim3 grid(static_cast<unsigned>(q_tokens / kRows + batch), static_cast<unsigned>(q.heads));
-  if (head_dim <= 64)
-    prompt_kernel<64><<<grid, kThreads, 0, stream>>>(a);
-  else
-    prompt_kernel<128><<<grid, kThreads, 0, stream>>>(a);
-  return cudaGetLastError();
+               two_heads ? kRows : 2 * kRows, two_heads ? q.heads / 2 : q.heads, scale * 1.4426950408889634f,
+               device_status_word()};
+  CUtensorMap mq, mk, mv;
+  // without any key no tile of k or v is ever loaded
+  *bad_args = !make_tmap_heads(&mq, q, head_dim, q_tokens, kRows) ||
+              !make_tmap_heads(&mk, k_tokens > 0 ? k : q, head_dim, k_tokens > 0 ? k_tokens : q_tokens, kKeys) ||
+              !make_tmap_heads(&mv, k_tokens > 0 ? v : q, head_dim, k_tokens > 0 ? k_tokens : q_tokens, kKeys);
+  if (*bad_args) return cudaSuccess;
+  const unsigned grid = static_cast<unsigned>((q_tokens / a.tile_rows + batch) * a.pairs);
+  return head_dim <= 64 ? launch_dim<64>(a, mq, mk, mv, grid, stream) : launch_dim<128>(a, mq, mk, mv, grid, stream);
 }
 
 }  // namespace svdq
