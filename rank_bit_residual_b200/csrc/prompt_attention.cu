@@ -26,7 +26,9 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <type_traits>
 
+#include "encode.cuh"
 #include "internal.h"
 #include "ptx.cuh"
 
@@ -147,6 +149,33 @@ __device__ __forceinline__ float ex2(float x) {
   return r;
 }
 
+__device__ __forceinline__ float max3_nan(float x, float y, float z) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
+  return r;
+}
+
+// 2^x of a pair on the FMA pipe, for x from -126 (and below, as -126) to 126: x = n + f with n
+// the nearest integer (added and subtracted 1.5 * 2^23 leaves it in the low bits), 2^f on
+// [-1/2, 1/2] by the cubic of least maximal relative error (7.5e-5, from an exchange
+// iteration; bf16 rounds to 2^-9 afterwards), and n added to the exponent.
+__device__ __forceinline__ uint64_t exp2_poly(uint64_t x) {
+  constexpr float kShift = 12582912.0f;
+  float lo, hi;
+  upk2(x, lo, hi);
+  x = pk2(fmaxf(lo, -126.0f), fmaxf(hi, -126.0f));
+  const uint64_t r = fadd2_rn(x, pk2(kShift, kShift));
+  const uint64_t f = fsub2_rn(x, fsub2_rn(r, pk2(kShift, kShift)));
+  uint64_t p = ffma2_rn(pk2(0.05517167f, 0.05517167f), f, pk2(0.24261112f, 0.24261112f));
+  p = ffma2_rn(p, f, pk2(0.69326099f, 0.69326099f));
+  p = ffma2_rn(p, f, pk2(0.99992807f, 0.99992807f));
+  float nl, nh, pl, ph;
+  upk2(r, nl, nh);
+  upk2(p, pl, ph);
+  return pk2(__uint_as_float((__float_as_uint(nl) << 23) + __float_as_uint(pl)),
+             __uint_as_float((__float_as_uint(nh) << 23) + __float_as_uint(ph)));
+}
+
 // The bf16 pairs of a word, infinities and NaN replaced by zero; sets *found then.
 __device__ __forceinline__ uint32_t finite_or_zero(uint32_t w, bool* found) {
   if ((w & 0x7F80u) == 0x7F80u) w &= 0xFFFF0000u, *found = true;
@@ -168,6 +197,7 @@ struct Shape {
   static constexpr int kTile = kKeys * kDim * 2;         // bytes of 128 rows of a head
   static constexpr int kRing = kDim == 128 ? 5 : 10;     // tiles of keys and values in flight
   static constexpr int kSmem = 2 * kTile + kRing * kTile + 1024;
+  static constexpr int kPoly = 0;      // pairs of eight whose exponentials go to the FMA pipe
   static constexpr int kO = 256;                         // tensor memory columns: S0, S1, O0, O1
 };
 
@@ -207,7 +237,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   unsigned char* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   unsigned char* sq = smem;              // two tiles of Q
   unsigned char* ring = smem + 2 * Sz::kTile;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   volatile int* abort = &abort_flag;
 
   if (threadIdx.x == 0) {
@@ -272,7 +302,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (index < 0) break;
         const int n = it.valid ? max(it.n[0], it.n[1]) : 0;
         if (ok && n > 0 && lane == 0) {
-          ok = mbar_wait(&bar.q_empty, q_phase ^ 1, a.status, abort);
+          ok = mbar_wait_soon(&bar.q_empty, q_phase ^ 1, a.status, abort);
           q_phase ^= 1;
           if (ok) {
             mbar_arrive_expect_tx(&bar.q_full, 2 * Sz::kTile);
@@ -283,7 +313,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tma_load_3d(sq + t * Sz::kTile + c * kRows * 128, &map_q, &bar.q_full, c * 64, it.head[t], it.row[t]);
           }
           for (int j = 0; ok && j < 2 * n; ++j) {   // K0, V0, K1, V1, ...
-            ok = mbar_wait(&bar.empty[r.i], r.phase ^ 1, a.status, abort);
+            ok = mbar_wait_soon(&bar.empty[r.i], r.phase ^ 1, a.status, abort);
             if (!ok) break;
             const bool raw = (j & 1) && (j >> 1) >= it.cut;
             uint64_t* to = raw ? &bar.raw[r.i] : &bar.full[r.i];
@@ -321,81 +351,102 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     } else if (warp == 8) {
       // ------------------------------------------------------------------ products
-      if (lane == 0) {
-        constexpr uint32_t idesc_s = idesc_bf16(kRows, kKeys), idesc_o = idesc_bf16_bmn(kRows, kDim);
-        Turn<kItems> slot;
-        Turn<Sz::kRing> r;
-        uint32_t q_phase = 0, p_phase[2] = {0, 0};
-        bool ok = true;
-        auto scores = [&](int t, int buf) {
-          const uint32_t qa = smem_u32(sq + t * Sz::kTile), kb = smem_u32(ring + buf * Sz::kTile);
+      // The whole warp walks through this part and one lane issues; what the instructions
+      // take is broadcast from lane 0, so that the compiler keeps it in uniform registers
+      // (an instruction whose operands it has to move there first takes about 60 cycles
+      // to issue, as long as it takes to run).
+      auto uniform = [](int x) { return __shfl_sync(0xffffffffu, x, 0); };
+      constexpr uint32_t idesc_o = idesc_bf16_bmn(kRows, kDim);
+      // a negative scale negates Q in the product (bit 13), so that softmax sees a positive one
+      const uint32_t idesc_s = idesc_bf16(kRows, kKeys) | (a.scale_log2 < 0.0f ? 1u << 13 : 0u);
+      const uint32_t tm = uniform(tmem);
+      const uint32_t q0 = uniform(smem_u32(sq)), ring0 = uniform(smem_u32(ring));
+      const bool leader = elect_one() != 0;
+      Turn<kItems> slot;
+      Turn<Sz::kRing> r;
+      uint32_t q_phase = 0, p_phase[2] = {0, 0};
+      bool ok = true;
+      auto scores = [&](int t, int buf) {
+        const uint64_t qd = smem_desc_sw128(q0 + t * Sz::kTile), kd = smem_desc_sw128(ring0 + buf * Sz::kTile);
+        if (leader) {
 #pragma unroll
           for (int kk = 0; kk < kDim / 16; ++kk) {
-            const uint32_t off = (kk >> 2) * (kRows * 128) + (kk & 3) * 32;
-            mma_f16(tmem + t * kKeys, smem_desc_sw128(qa + off), smem_desc_sw128(kb + off), idesc_s, kk > 0);
+            const uint64_t off = ((kk >> 2) * (kRows * 128) + (kk & 3) * 32) >> 4;
+            mma_f16(tm + t * kKeys, qd + off, kd + off, idesc_s, kk > 0);
           }
           mma_commit(&bar.s_full[t]);
-        };
-        while (true) {
-          ok = mbar_wait(&bar.item_full[slot.i], slot.phase, a.status, abort);
-          if (!ok) break;
-          const Item it = items[slot.i];
-          mbar_arrive(&bar.item_empty[slot.i]);
-          slot.next();
-          if (!it.valid) break;
-          const int n = max(it.n[0], it.n[1]);
-          if (n == 0) continue;
-          ok = mbar_wait(&bar.q_full, q_phase, a.status, abort) && mbar_wait(&bar.full[r.i], r.phase, a.status, abort);
-          q_phase ^= 1;
-          if (!ok) break;
-          tc_fence_after();
+        }
+        __syncwarp();
+      };
+      auto commit = [&](uint64_t* b) {
+        if (leader) mma_commit(b);
+        __syncwarp();
+      };
+      while (true) {
+        if (!mbar_wait_soon_warp(&bar.item_full[slot.i], slot.phase, a.status, abort)) break;
+        const int valid = uniform(items[slot.i].valid);
+        const int n0 = uniform(items[slot.i].n[0]), n1 = uniform(items[slot.i].n[1]);
+        if (leader) mbar_arrive(&bar.item_empty[slot.i]);
+        __syncwarp();
+        slot.next();
+        if (!valid) break;
+        const int n = max(n0, n1);
+        if (n == 0) continue;
+        ok = mbar_wait_soon_warp(&bar.q_full, q_phase, a.status, abort) &&
+             mbar_wait_soon_warp(&bar.full[r.i], r.phase, a.status, abort);
+        q_phase ^= 1;
+        if (!ok) break;
+        tc_fence_after();
 #pragma unroll
-          for (int t = 0; t < 2; ++t)
-            if (it.n[t] > 0) scores(t, r.i);
-          mma_commit(&bar.empty[r.i]);
-          if (n == 1) mma_commit(&bar.q_empty);
+        for (int t = 0; t < 2; ++t)
+          if ((t ? n1 : n0) > 0) scores(t, r.i);
+        commit(&bar.empty[r.i]);
+        if (n == 1) commit(&bar.q_empty);
+        r.next();
+        for (int j = 0; ok && j < n; ++j) {
+          const int vbuf = r.i;
+          ok = mbar_wait_soon_warp(&bar.full[vbuf], r.phase, a.status, abort);
           r.next();
-          for (int j = 0; ok && j < n; ++j) {
-            const int vbuf = r.i;
-            ok = mbar_wait(&bar.full[vbuf], r.phase, a.status, abort);
-            r.next();
-            const bool more = j + 1 < n;
-            const int kbuf = r.i;
-            bool have_k = false;
-            const uint32_t vb = smem_u32(ring + vbuf * Sz::kTile);
+          const bool more = j + 1 < n;
+          const int kbuf = r.i;
+          bool have_k = false;
+          const uint64_t vd = smem_desc_sw128_mn(ring0 + vbuf * Sz::kTile, kKeys * 128);
 #pragma unroll
-            for (int t = 0; t < 2; ++t) {
-              if (ok && j < it.n[t]) {
-                ok = mbar_wait(&bar.p_full[t], p_phase[t], a.status, abort);
-                p_phase[t] ^= 1;
-                if (ok) {
-                  tc_fence_after();
+          for (int t = 0; t < 2; ++t) {
+            const int nt = t ? n1 : n0;
+            if (ok && j < nt) {
+              ok = mbar_wait_soon_warp(&bar.p_full[t], p_phase[t], a.status, abort);
+              p_phase[t] ^= 1;
+              if (ok) {
+                tc_fence_after();
+                if (leader) {
 #pragma unroll
                   for (int kk = 0; kk < kKeys / 16; ++kk)
-                    mma_f16_ta(tmem + Sz::kO + t * kDim, tmem + t * kKeys + kk * 8,
-                               smem_desc_sw128_mn(vb + kk * 2048, kKeys * 128), idesc_o, j > 0 || kk > 0);
-                  if (j == it.n[t] - 1) mma_commit(&bar.o_full[t]);
+                    mma_f16_ta(tm + Sz::kO + t * kDim, tm + t * kKeys + kk * 8, vd + ((kk * 2048) >> 4), idesc_o,
+                               j > 0 || kk > 0);
+                  if (j == nt - 1) mma_commit(&bar.o_full[t]);
                 }
-              }
-              if (ok && j + 1 < it.n[t]) {
-                if (!have_k) {
-                  ok = mbar_wait(&bar.full[kbuf], r.phase, a.status, abort);
-                  have_k = true;
-                  tc_fence_after();
-                }
-                if (ok) scores(t, kbuf);
+                __syncwarp();
               }
             }
-            if (!ok) break;
-            mma_commit(&bar.empty[vbuf]);
-            if (more) {
-              mma_commit(&bar.empty[kbuf]);
-              if (j + 2 == n) mma_commit(&bar.q_empty);
-              r.next();
+            if (ok && j + 1 < nt) {
+              if (!have_k) {
+                ok = mbar_wait_soon_warp(&bar.full[kbuf], r.phase, a.status, abort);
+                have_k = true;
+                tc_fence_after();
+              }
+              if (ok) scores(t, kbuf);
             }
           }
           if (!ok) break;
+          commit(&bar.empty[vbuf]);
+          if (more) {
+            commit(&bar.empty[kbuf]);
+            if (j + 2 == n) commit(&bar.q_empty);
+            r.next();
+          }
         }
+        if (!ok) break;
       }
     } else if (warp == 10) {
       // ----------------------------------------------------------------- cleaning
@@ -452,7 +503,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int row = (warp & 3) * 32 + lane;   // of the tile
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t ts = tmem + lanes + t * kKeys, to = tmem + lanes + Sz::kO + t * kDim;
-    // The scores take the sign. A scale of zero is one so small that all weights are 1, and
+    // The product takes the sign. A scale of zero is one so small that all weights are 1, and
     // a masked -inf still comes out as a weight of 0.
     const float scale = fmaxf(fabsf(a.scale_log2), 1e-30f);
     Turn<kItems> slot;
@@ -470,72 +521,88 @@ __global__ void __launch_bounds__(kThreads, 1)
       slot.next();
       if (!valid) break;
       ++number;
-      float m = -INFINITY, l = 0.0f;
+      float m = -INFINITY;
+      uint64_t sums[2] = {0, 0};   // two pairs of partial sums
       bool ok = true;
       for (int j = 0; j < n; ++j) {
-        ok = mbar_wait(&bar.s_full[t], s_phase, a.status, abort);
-        ok = __all_sync(0xffffffffu, ok);
+        ok = mbar_wait_soon_warp(&bar.s_full[t], s_phase, a.status, abort);
         if (!ok) break;
         s_phase ^= 1;
         tc_fence_after();
-        uint32_t s[kKeys / 32][32];
-#pragma unroll
-        for (int c = 0; c < kKeys / 32; ++c) tmem_ld_32x32b_x32(ts + c * 32, s[c]);
-        tmem_ld_wait();
-#pragma unroll
-        for (int c = 0; c < kKeys / 32; ++c)
-#pragma unroll
-          for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(s[c][i]));
-        if (a.scale_log2 < 0.0f) {
-#pragma unroll
-          for (int c = 0; c < kKeys / 32; ++c)
-#pragma unroll
-            for (int i = 0; i < 32; ++i) s[c][i] ^= 0x80000000u;
-        }
-        if ((j + 1) * kKeys > all_see) {
+        // kMasked: some row of the tile does not see all of these keys
+        auto softmax = [&](auto masked) {
+          constexpr bool kMasked = decltype(masked)::value;
+          uint32_t s[kKeys / 32][32];
           const int left = seen - j * kKeys;
+          float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+          tmem_ld_32x32b_x32(ts, s[0]);
 #pragma unroll
-          for (int c = 0; c < kKeys / 32; ++c)
+          for (int c = 0; c < kKeys / 32; ++c) {
+            tmem_ld_wait_regs(s[c]);
+            if (c + 1 < kKeys / 32) tmem_ld_32x32b_x32(ts + (c + 1) * 32, s[c + 1]);
+            if (kMasked) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (c * 32 + i >= left) s[c][i] = 0xFF800000u;   // -inf
-        }
-        float top = -INFINITY;
+              for (int i = 0; i < 32; ++i)
+                if (c * 32 + i >= left) s[c][i] = 0xFF800000u;   // -inf
+            }
 #pragma unroll
-        for (int c = 0; c < kKeys / 32; ++c)
+            for (int i = 0; i < 32; i += 2)
+              tops[(i >> 1) & 3] = max3_nan(tops[(i >> 1) & 3], __uint_as_float(s[c][i]), __uint_as_float(s[c][i + 1]));
+          }
+          const float top = max3_nan(max3_nan(tops[0], tops[1], tops[2]), tops[3], tops[3]) * scale;
+          if (__any_sync(0xffffffffu, top > m + 8.0f || (m == -INFINITY && top > m))) {
+            const float up = fmaxf(m, top);
+            const float f = m == -INFINITY ? 0.0f : ex2(m - up);
+            m = up;
+            sums[0] = fmul2_rn(sums[0], pk2(f, f));
+            sums[1] = fmul2_rn(sums[1], pk2(f, f));
+            if (j > 0) {
+#pragma unroll 1
+              for (int c = 0; c < kDim / 16; ++c) {
+                uint32_t o[16];
+                tmem_ld_32x32b_x16(to + c * 16, o);
+                tmem_ld_wait_regs(o);
 #pragma unroll
-          for (int i = 0; i < 32; ++i) top = fmaxf(top, __uint_as_float(s[c][i]));
-        top *= scale;
-        if (__any_sync(0xffffffffu, top > m + 8.0f || (m == -INFINITY && top > m))) {
-          const float up = fmaxf(m, top);
-          const float f = m == -INFINITY ? 0.0f : ex2(m - up);
-          m = up;
-          l *= f;
-          if (j > 0) {
-#pragma unroll
-            for (int c = 0; c < kDim / 32; ++c) {
-              uint32_t o[32];
-              tmem_ld_32x32b_x32(to + c * 32, o);
-              tmem_ld_wait_regs(o);
-#pragma unroll
-              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-              tmem_st_32x32b_x32(to + c * 32, o);
+                for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                tmem_st_32x32b_x16(to + c * 16, o);
+              }
             }
           }
-        }
-        const float base = m == -INFINITY ? 0.0f : -m;
+          const float base = m == -INFINITY ? 0.0f : -m;
+          const uint64_t scale2 = pk2(scale, scale), base2 = pk2(base, base);
+          auto weights = [&](auto poly) {
 #pragma unroll
-        for (int c = 0; c < kKeys / 32; ++c) {
-          uint32_t p[16];
+            for (int c = 0; c < kKeys / 32; ++c) {
+              uint32_t p[16];
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const float x = ex2(fmaf(__uint_as_float(s[c][2 * i]), scale, base));
-            const float y = ex2(fmaf(__uint_as_float(s[c][2 * i + 1]), scale, base));
-            l += x + y;
-            p[i] = pack_bf16(x, y);
-          }
-          tmem_st_32x32b_x16(ts + c * 16, p);
-        }
+              for (int i = 0; i < 16; ++i) {
+                const uint64_t x =
+                    ffma2_rn(pk2(__uint_as_float(s[c][2 * i]), __uint_as_float(s[c][2 * i + 1])), scale2, base2);
+                uint64_t e;
+                float lo, hi;
+                if (i % 8 >= 8 - decltype(poly)::value) {
+                  e = exp2_poly(x);
+                } else {
+                  upk2(x, lo, hi);
+                  e = pk2(ex2(lo), ex2(hi));
+                }
+                sums[i & 1] = fadd2_rn(sums[i & 1], e);
+                upk2(e, lo, hi);
+                p[i] = pack_bf16(lo, hi);
+              }
+              tmem_st_32x32b_x16(ts + c * 16, p);
+            }
+          };
+          // the polynomial takes neither NaN nor -inf
+          if (kMasked || Sz::kPoly == 0 || __any_sync(0xffffffffu, !(top > -INFINITY)))
+            weights(std::integral_constant<int, 0>{});
+          else
+            weights(std::integral_constant<int, Sz::kPoly>{});
+        };
+        if ((j + 1) * kKeys > all_see)
+          softmax(std::true_type{});
+        else
+          softmax(std::false_type{});
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
@@ -543,12 +610,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!ok) break;
       if (n > 0) {
-        ok = mbar_wait(&bar.o_full[t], o_phase, a.status, abort);
-        ok = __all_sync(0xffffffffu, ok);
+        ok = mbar_wait_soon_warp(&bar.o_full[t], o_phase, a.status, abort);
         if (!ok) break;
         o_phase ^= 1;
         tc_fence_after();
       }
+      float l4[4];
+      upk2(sums[0], l4[0], l4[1]);
+      upk2(sums[1], l4[2], l4[3]);
+      const float l = (l4[0] + l4[1]) + (l4[2] + l4[3]);
       const float inv = l == 0.0f ? 0.0f : 1.0f / l;
       const bool extra = n > 0 && odd[number % (2 * kItems)] == number;
       __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.out.data) +

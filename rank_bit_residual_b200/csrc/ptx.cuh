@@ -97,6 +97,17 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, unsign
   }
 }
 
+// The same for waits on a critical path of a few hundred cycles: some suspending polls
+// come first (each ends after about a millisecond at the latest), because reading the
+// wall clock takes longer than such a wait does.
+__device__ __forceinline__ bool mbar_wait_soon(uint64_t* bar, uint32_t parity, unsigned* status,
+                                               volatile int* abort) {
+#pragma unroll 1
+  for (int i = 0; i < 4; ++i)
+    if (mbar_try_wait_sleep(bar, parity)) return true;
+  return mbar_wait(bar, parity, status, abort);
+}
+
 // Warp-wide wait (call with the warp converged): lane 0 polls the barrier and
 // the result is broadcast, so a waiting warp puts one poller on the
 // shared-memory pipe instead of 32; the warp barrier after the poll orders the
@@ -109,6 +120,12 @@ __device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, u
   ok = __shfl_sync(0xffffffffu, ok, 0);
   __syncwarp();
   return ok != 0;
+}
+
+// The same for a converged warp, every lane polling: no lane has to hand the answer on.
+__device__ __forceinline__ bool mbar_wait_soon_warp(uint64_t* bar, uint32_t parity, unsigned* status,
+                                                    volatile int* abort) {
+  return __all_sync(0xffffffffu, mbar_wait_soon(bar, parity, status, abort));
 }
 
 // ----------------------------------------------------------------------- TMA
