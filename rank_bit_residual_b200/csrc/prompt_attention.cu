@@ -4,20 +4,23 @@
 //
 // One pass over the keys with a running maximum and sum. A block works on an item of two
 // tiles of 128 query rows that share their keys: the same rows of two query heads of one
-// key head when the group is even, else 256 consecutive rows of one head. Per tile of 128
-// keys and 128 rows, S = Q K^T goes to tensor memory, four warps (one row per
-// thread, so row maxima and sums need no exchange) turn it into P = 2^(S c - m) in bf16
-// and put it back over S, and O += P V accumulates in tensor memory with P as the operand
-// from there. While one tile's S is in softmax, the tensor cores work on the other's
-// products: with 128-element heads a tile costs 1024 cycles of products and 1024 of
+// key head when the group is even, else 256 consecutive rows of one head. Per tile and 64
+// keys, S = Q K^T goes to tensor memory, four warps (one row per thread, so row maxima
+// and sums need no exchange) turn it into P = 2^(S c - m) in bf16 and put it back over
+// S, and O += P V accumulates in tensor memory with P as the operand from there. Each
+// tile has two S buffers: the products of the next 64 keys run while softmax works on
+// these. (With one buffer of 128 keys, softmax waited for P V and the next S in turn: 3400
+// cycles per 128 keys of both tiles against 2048 of products.)
+//
+// With 128-element heads a tile of 128 keys costs 1024 cycles of products and 1024 of
 // exponentials (16 a cycle), so both bound the kernel.
 //
 // The maximum is renewed (and O rescaled, by the softmax warps themselves) only when a
-// score passes it by 2^8; P then stays below 2^8, and both sums are fp32. Because
-// products run in order, S(j) complete means that O holds all tiles before j: no further
-// barrier guards the rescaling.
+// score passes it by 2^8; P then stays below 2^8, and both sums are fp32. O is at rest for
+// that once the products of the next S are complete, because products run in order and
+// that S follows P V of the keys before these.
 //
-// Warps: 0-3 and 4-7 softmax and output of the two tiles, 8 the products, 9 the loads and the
+// Warps: 0-3 and 4-7 softmax and output of the two tiles, 8 and 11 their products, 9 the loads and the
 // choice of items (blocks that have not started are taken over, so that long and short
 // items balance), 10 cleans values: in tiles that hold a key some row does not see,
 // rows behind the sequence's end become zero, and infinities and NaN too (a zero weight
@@ -37,10 +40,10 @@ namespace svdq {
 namespace {
 
 constexpr int kRows = 128;      // query rows of a tile
-constexpr int kKeys = 128;      // keys of a tile
+constexpr int kKeys = 128;      // keys of a loaded tile
+constexpr int kPart = 64;       // keys of a part: what softmax takes at a time
 constexpr int kThreads = 384;
 constexpr int kItems = 4;       // items between the chooser and the slowest reader
-constexpr int kSoftmaxRegs = 216, kOtherRegs = 72;   // 256 * 216 + 128 * 72 = 384 * 168
 
 struct PromptArgs {
   svdq_heads q, k, v, out;
@@ -59,8 +62,8 @@ struct Item {
   int valid;        // 0: no more
   int keys, k0;     // keys of the sequence and their first row
   int kvh;
-  int n[2];         // key tiles of each row tile
-  int cut;          // first key tile with a key that some row does not see
+  int n[2];         // parts of each row tile
+  int cut;          // first loaded tile with a key that some row does not see
   int row[2];       // first row in q and out
   int rows[2];      // rows inside the sequence, 0 .. 128
   int head[2];
@@ -126,7 +129,7 @@ __device__ Item find_item(const PromptArgs& a, int index) {
         it.rows[t] = max(0, min(kRows, rows - row));
         it.seen[t] = a.causal ? keys - rows + row + 1 : keys;
         const int last = a.causal ? min(keys, it.seen[t] + it.rows[t] - 1) : keys;
-        it.n[t] = it.rows[t] > 0 ? max(0, last + kKeys - 1) / kKeys : 0;
+        it.n[t] = it.rows[t] > 0 ? max(0, last + kPart - 1) / kPart : 0;
         it.cut = min(it.cut, max(0, min(keys, it.seen[t])) / kKeys);
       }
       it.kvh = it.head[0] / (a.q.heads / a.k.heads);
@@ -183,21 +186,12 @@ __device__ __forceinline__ uint32_t finite_or_zero(uint32_t w, bool* found) {
   return w;
 }
 
-template <int kRegs>
-__device__ __forceinline__ void regs_up() {
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
-}
-template <int kRegs>
-__device__ __forceinline__ void regs_down() {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
-}
-
 template <int kDim>
 struct Shape {
   static constexpr int kTile = kKeys * kDim * 2;         // bytes of 128 rows of a head
   static constexpr int kRing = kDim == 128 ? 5 : 10;     // tiles of keys and values in flight
   static constexpr int kSmem = 2 * kTile + kRing * kTile + 1024;
-  static constexpr int kPoly = 0;      // pairs of eight whose exponentials go to the FMA pipe
+  static constexpr int kPoly = 1;      // pairs of eight whose exponentials go to the FMA pipe
   static constexpr int kO = 256;                         // tensor memory columns: S0, S1, O0, O1
 };
 
@@ -206,7 +200,7 @@ struct Barriers {
   uint64_t q_full, q_empty;
   uint64_t full[kRing], empty[kRing];
   uint64_t raw[kRing];   // loaded, for the cleaning warp, which then completes `full`
-  uint64_t s_full[2], p_full[2], o_full[2];
+  uint64_t s_full[2][2], p_full[2][2], o_full[2];   // by row tile and buffer
   uint64_t item_full[kItems], item_empty[kItems];
   uint64_t answer;
 };
@@ -243,20 +237,22 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     abort_flag = 0;
     mbar_init(&bar.q_full, 1);
-    mbar_init(&bar.q_empty, 1);
+    mbar_init(&bar.q_empty, 2);
     for (int i = 0; i < Sz::kRing; ++i) {
       mbar_init(&bar.full[i], 1);
-      mbar_init(&bar.empty[i], 1);
+      mbar_init(&bar.empty[i], 2);
       mbar_init(&bar.raw[i], 1);
     }
     for (int t = 0; t < 2; ++t) {
-      mbar_init(&bar.s_full[t], 1);
-      mbar_init(&bar.p_full[t], 4);
+      for (int b = 0; b < 2; ++b) {
+        mbar_init(&bar.s_full[t][b], 1);
+        mbar_init(&bar.p_full[t][b], 4);
+      }
       mbar_init(&bar.o_full[t], 1);
     }
     for (int i = 0; i < kItems; ++i) {
       mbar_init(&bar.item_full[i], 1);
-      mbar_init(&bar.item_empty[i], 10);   // 8 softmax warps, the products, the cleaning warp
+      mbar_init(&bar.item_empty[i], 11);   // 8 softmax warps, 2 for the products, the cleaning warp
       odd[i] = odd[kItems + i] = 0;
     }
     mbar_init(&bar.answer, 1);
@@ -272,9 +268,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_base;
+  __syncwarp();   // .aligned instructions follow in every role
 
   if (warp >= 8) {
-    regs_down<kOtherRegs>();
     if (warp == 9) {
       // ---------------------------------------------------------- items and loads
       Turn<kItems> slot;
@@ -300,7 +296,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           slot.next();
         }
         if (index < 0) break;
-        const int n = it.valid ? max(it.n[0], it.n[1]) : 0;
+        const int n = it.valid ? (max(it.n[0], it.n[1]) + 1) / 2 : 0;   // tiles of two parts
         if (ok && n > 0 && lane == 0) {
           ok = mbar_wait_soon(&bar.q_empty, q_phase ^ 1, a.status, abort);
           q_phase ^= 1;
@@ -349,8 +345,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           w.next();
         }
       }
-    } else if (warp == 8) {
+    } else if (warp == 8 || warp == 11) {
       // ------------------------------------------------------------------ products
+      // One warp for each row tile, so that one's waits do not hold up the other's products.
       // The whole warp walks through this part and one lane issues; what the instructions
       // take is broadcast from lane 0, so that the compiler keeps it in uniform registers
       // (an instruction whose operands it has to move there first takes about 60 cycles
@@ -358,93 +355,88 @@ __global__ void __launch_bounds__(kThreads, 1)
       auto uniform = [](int x) { return __shfl_sync(0xffffffffu, x, 0); };
       constexpr uint32_t idesc_o = idesc_bf16_bmn(kRows, kDim);
       // a negative scale negates Q in the product (bit 13), so that softmax sees a positive one
-      const uint32_t idesc_s = idesc_bf16(kRows, kKeys) | (a.scale_log2 < 0.0f ? 1u << 13 : 0u);
+      const uint32_t idesc_s = idesc_bf16(kRows, kPart) | (a.scale_log2 < 0.0f ? 1u << 13 : 0u);
+      const int t = warp == 8 ? 0 : 1;
       const uint32_t tm = uniform(tmem);
-      const uint32_t q0 = uniform(smem_u32(sq)), ring0 = uniform(smem_u32(ring));
+      const uint32_t q0 = uniform(smem_u32(sq)) + t * Sz::kTile, ring0 = uniform(smem_u32(ring));
+      const uint32_t ts = tm + t * kKeys, to = tm + Sz::kO + t * kDim;
       const bool leader = elect_one() != 0;
       Turn<kItems> slot;
       Turn<Sz::kRing> r;
-      uint32_t q_phase = 0, p_phase[2] = {0, 0};
+      uint32_t q_phase = 0, p_phase = 0;   // the latter with a bit per buffer
       bool ok = true;
-      auto scores = [&](int t, int buf) {
-        const uint64_t qd = smem_desc_sw128(q0 + t * Sz::kTile), kd = smem_desc_sw128(ring0 + buf * Sz::kTile);
+      auto commit = [&](uint64_t* b) {
+        if (leader) mma_commit(b);
+        __syncwarp();
+      };
+      // S of part i, from the keys in ring position buf
+      auto scores = [&](int i, int buf) {
+        const uint64_t qd = smem_desc_sw128(q0);
+        const uint64_t kd = smem_desc_sw128(ring0 + buf * Sz::kTile + (i & 1) * (kPart * 128));
         if (leader) {
 #pragma unroll
           for (int kk = 0; kk < kDim / 16; ++kk) {
             const uint64_t off = ((kk >> 2) * (kRows * 128) + (kk & 3) * 32) >> 4;
-            mma_f16(tm + t * kKeys, qd + off, kd + off, idesc_s, kk > 0);
+            mma_f16(ts + (i & 1) * kPart, qd + off, kd + off, idesc_s, kk > 0);
           }
-          mma_commit(&bar.s_full[t]);
+          mma_commit(&bar.s_full[t][i & 1]);
         }
-        __syncwarp();
-      };
-      auto commit = [&](uint64_t* b) {
-        if (leader) mma_commit(b);
         __syncwarp();
       };
       while (true) {
         if (!mbar_wait_soon_warp(&bar.item_full[slot.i], slot.phase, a.status, abort)) break;
         const int valid = uniform(items[slot.i].valid);
-        const int n0 = uniform(items[slot.i].n[0]), n1 = uniform(items[slot.i].n[1]);
+        const int n = uniform(items[slot.i].n[t]);                                // parts of this tile
+        const int both = uniform(max(items[slot.i].n[0], items[slot.i].n[1]));   // parts that are loaded
         if (leader) mbar_arrive(&bar.item_empty[slot.i]);
         __syncwarp();
         slot.next();
         if (!valid) break;
-        const int n = max(n0, n1);
-        if (n == 0) continue;
+        if (both == 0) continue;
         ok = mbar_wait_soon_warp(&bar.q_full, q_phase, a.status, abort) &&
              mbar_wait_soon_warp(&bar.full[r.i], r.phase, a.status, abort);
         q_phase ^= 1;
         if (!ok) break;
         tc_fence_after();
 #pragma unroll
-        for (int t = 0; t < 2; ++t)
-          if ((t ? n1 : n0) > 0) scores(t, r.i);
+        for (int i = 0; i < 2; ++i)
+          if (i < n) scores(i, r.i);
         commit(&bar.empty[r.i]);
-        if (n == 1) commit(&bar.q_empty);
+        if (both <= 2) commit(&bar.q_empty);
         r.next();
-        for (int j = 0; ok && j < n; ++j) {
-          const int vbuf = r.i;
-          ok = mbar_wait_soon_warp(&bar.full[vbuf], r.phase, a.status, abort);
-          r.next();
-          const bool more = j + 1 < n;
-          const int kbuf = r.i;
-          bool have_k = false;
-          const uint64_t vd = smem_desc_sw128_mn(ring0 + vbuf * Sz::kTile, kKeys * 128);
-#pragma unroll
-          for (int t = 0; t < 2; ++t) {
-            const int nt = t ? n1 : n0;
-            if (ok && j < nt) {
-              ok = mbar_wait_soon_warp(&bar.p_full[t], p_phase[t], a.status, abort);
-              p_phase[t] ^= 1;
-              if (ok) {
-                tc_fence_after();
-                if (leader) {
-#pragma unroll
-                  for (int kk = 0; kk < kKeys / 16; ++kk)
-                    mma_f16_ta(tm + Sz::kO + t * kDim, tm + t * kKeys + kk * 8, vd + ((kk * 2048) >> 4), idesc_o,
-                               j > 0 || kk > 0);
-                  if (j == nt - 1) mma_commit(&bar.o_full[t]);
-                }
-                __syncwarp();
-              }
-            }
-            if (ok && j + 1 < nt) {
-              if (!have_k) {
-                ok = mbar_wait_soon_warp(&bar.full[kbuf], r.phase, a.status, abort);
-                have_k = true;
-                tc_fence_after();
-              }
-              if (ok) scores(t, kbuf);
-            }
-          }
-          if (!ok) break;
-          commit(&bar.empty[vbuf]);
-          if (more) {
-            commit(&bar.empty[kbuf]);
-            if (j + 2 == n) commit(&bar.q_empty);
+        int vbuf = 0, kbuf = 0;
+        for (int i = 0; i < both; ++i) {
+          if ((i & 1) == 0) {
+            vbuf = r.i;
+            ok = mbar_wait_soon_warp(&bar.full[vbuf], r.phase, a.status, abort);
             r.next();
+            if (ok && i + 2 < both) {
+              kbuf = r.i;
+              ok = mbar_wait_soon_warp(&bar.full[kbuf], r.phase, a.status, abort);
+              r.next();
+            }
+            if (!ok) break;
           }
+          if (i < n) {
+            ok = mbar_wait_soon_warp(&bar.p_full[t][i & 1], (p_phase >> (i & 1)) & 1, a.status, abort);
+            if (!ok) break;
+            p_phase ^= 1u << (i & 1);
+            tc_fence_after();
+            const uint64_t vd = smem_desc_sw128_mn(ring0 + vbuf * Sz::kTile + (i & 1) * (kPart * 128), kKeys * 128);
+            if (leader) {
+#pragma unroll
+              for (int kk = 0; kk < kPart / 16; ++kk)
+                mma_f16_ta(to, ts + (i & 1) * kPart + kk * 8, vd + ((kk * 2048) >> 4), idesc_o, i > 0 || kk > 0);
+              if (i == n - 1) mma_commit(&bar.o_full[t]);
+              // in the place of the S that would come next: O is at rest for the last part
+              if (i == n - 2) mma_commit(&bar.s_full[t][i & 1]);
+            }
+            __syncwarp();
+            if (i + 2 < n) scores(i + 2, kbuf);
+          }
+          if ((i & 1) == 1 || i == both - 1) commit(&bar.empty[vbuf]);
+          if (i + 2 < both && ((i & 1) == 1 || i + 3 == both)) commit(&bar.empty[kbuf]);
+          if (i + 3 == both) commit(&bar.q_empty);
         }
         if (!ok) break;
       }
@@ -462,7 +454,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         slot.next();
         if (!it.valid) break;
         ++number;
-        const int n = max(it.n[0], it.n[1]);
+        const int n = (max(it.n[0], it.n[1]) + 1) / 2;
         bool ok = true;
         for (int j = 0; ok && j < n; ++j) {
           r.next();                        // the keys
@@ -498,16 +490,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     // ------------------------------------------------------------ softmax and output
-    regs_up<kSoftmaxRegs>();
     const int t = warp >> 2;
     const int row = (warp & 3) * 32 + lane;   // of the tile
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t ts = tmem + lanes + t * kKeys, to = tmem + lanes + Sz::kO + t * kDim;
+    const uint32_t to = tmem + lanes + Sz::kO + t * kDim;
     // The product takes the sign. A scale of zero is one so small that all weights are 1, and
     // a masked -inf still comes out as a weight of 0.
     const float scale = fmaxf(fabsf(a.scale_log2), 1e-30f);
     Turn<kItems> slot;
-    uint32_t s_phase = 0, o_phase = 0;
+    uint32_t s_phase = 0, o_phase = 0;   // the former with a bit per buffer
     int number = 0;
     while (true) {
       if (!mbar_wait_warp(&bar.item_full[slot.i], slot.phase, a.status, abort)) break;
@@ -525,90 +516,103 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint64_t sums[2] = {0, 0};   // two pairs of partial sums
       bool ok = true;
       for (int j = 0; j < n; ++j) {
-        ok = mbar_wait_soon_warp(&bar.s_full[t], s_phase, a.status, abort);
+        const int buf = j & 1;
+        const uint32_t ts = tmem + lanes + t * kKeys + buf * kPart;
+        ok = mbar_wait_soon_warp(&bar.s_full[t][buf], (s_phase >> buf) & 1, a.status, abort);
         if (!ok) break;
-        s_phase ^= 1;
+        s_phase ^= 1u << buf;
         tc_fence_after();
-        // kMasked: some row of the tile does not see all of these keys
-        auto softmax = [&](auto masked) {
-          constexpr bool kMasked = decltype(masked)::value;
-          uint32_t s[kKeys / 32][32];
-          const int left = seen - j * kKeys;
-          float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-          tmem_ld_32x32b_x32(ts, s[0]);
+        uint32_t s[2][32];
+        tmem_ld_32x32b_x32(ts, s[0]);
+        tmem_ld_wait_regs(s[0]);
+        tmem_ld_32x32b_x32(ts + 32, s[1]);
+        // weights of half a part with the maximum m; kPoly pairs of eight by polynomial
+        auto weights = [&](int c, auto poly, uint64_t scale2, uint64_t base2, uint64_t (&add)[2]) {
+          uint32_t p[16];
 #pragma unroll
-          for (int c = 0; c < kKeys / 32; ++c) {
-            tmem_ld_wait_regs(s[c]);
-            if (c + 1 < kKeys / 32) tmem_ld_32x32b_x32(ts + (c + 1) * 32, s[c + 1]);
-            if (kMasked) {
-#pragma unroll
-              for (int i = 0; i < 32; ++i)
-                if (c * 32 + i >= left) s[c][i] = 0xFF800000u;   // -inf
+          for (int i = 0; i < 16; ++i) {
+            const uint64_t x =
+                ffma2_rn(pk2(__uint_as_float(s[c][2 * i]), __uint_as_float(s[c][2 * i + 1])), scale2, base2);
+            uint64_t e;
+            float lo, hi;
+            if (i % 8 >= 8 - decltype(poly)::value) {
+              e = exp2_poly(x);
+            } else {
+              upk2(x, lo, hi);
+              e = pk2(ex2(lo), ex2(hi));
             }
-#pragma unroll
-            for (int i = 0; i < 32; i += 2)
-              tops[(i >> 1) & 3] = max3_nan(tops[(i >> 1) & 3], __uint_as_float(s[c][i]), __uint_as_float(s[c][i + 1]));
+            add[i & 1] = fadd2_rn(add[i & 1], e);
+            upk2(e, lo, hi);
+            p[i] = pack_bf16(lo, hi);
           }
-          const float top = max3_nan(max3_nan(tops[0], tops[1], tops[2]), tops[3], tops[3]) * scale;
-          if (__any_sync(0xffffffffu, top > m + 8.0f || (m == -INFINITY && top > m))) {
-            const float up = fmaxf(m, top);
-            const float f = m == -INFINITY ? 0.0f : ex2(m - up);
-            m = up;
-            sums[0] = fmul2_rn(sums[0], pk2(f, f));
-            sums[1] = fmul2_rn(sums[1], pk2(f, f));
-            if (j > 0) {
-#pragma unroll 1
-              for (int c = 0; c < kDim / 16; ++c) {
-                uint32_t o[16];
-                tmem_ld_32x32b_x16(to + c * 16, o);
-                tmem_ld_wait_regs(o);
+          tmem_st_32x32b_x16(ts + c * 16, p);
+        };
+        auto largest = [&](int c, float (&tops)[2]) {
 #pragma unroll
-                for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-                tmem_st_32x32b_x16(to + c * 16, o);
-              }
+          for (int i = 0; i < 32; i += 2)
+            tops[(i >> 1) & 1] = max3_nan(tops[(i >> 1) & 1], __uint_as_float(s[c][i]), __uint_as_float(s[c][i + 1]));
+        };
+        const uint64_t scale2 = pk2(scale, scale);
+        bool done = false;
+        if (j > 0 && (j + 1) * kPart <= all_see) {
+          // Most parts leave the maximum as it is: their weights are taken with it while their
+          // own largest score is found, and taken again in the rare case that it is too large (or NaN).
+          const uint64_t base2 = pk2(-m, -m);
+          uint64_t add[2] = {sums[0], sums[1]};
+          float tops[2] = {-INFINITY, -INFINITY};
+          largest(0, tops);
+          weights(0, std::integral_constant<int, Sz::kPoly>{}, scale2, base2, add);
+          tmem_ld_wait_regs(s[1]);
+          largest(1, tops);
+          weights(1, std::integral_constant<int, Sz::kPoly>{}, scale2, base2, add);
+          // (a row that has seen nothing but -inf, m = -inf, is not done either)
+          const float top = max3_nan(tops[0], tops[1], tops[1]) * scale;
+          done = __all_sync(0xffffffffu, top <= m + 8.0f && m > -INFINITY);
+          if (done) sums[0] = add[0], sums[1] = add[1];
+        } else {
+          tmem_ld_wait_regs(s[1]);
+        }
+        if (!done) {
+          const int left = seen - j * kPart;
+#pragma unroll
+          for (int c = 0; c < 2; ++c)
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (c * 32 + i >= left) s[c][i] = 0xFF800000u;   // -inf
+          float tops[2] = {-INFINITY, -INFINITY};
+          largest(0, tops);
+          largest(1, tops);
+          const float up = fmaxf(m, max3_nan(tops[0], tops[1], tops[1]) * scale);
+          const float f = m == -INFINITY ? 0.0f : ex2(m - up);
+          m = up;
+          sums[0] = fmul2_rn(sums[0], pk2(f, f));
+          sums[1] = fmul2_rn(sums[1], pk2(f, f));
+          if (j > 0 && __any_sync(0xffffffffu, f != 1.0f)) {
+            // O is at rest once the next S (or what stands for it) is complete
+            ok = mbar_wait_soon_warp(&bar.s_full[t][buf ^ 1], (s_phase >> (buf ^ 1)) & 1, a.status, abort);
+            if (!ok) break;
+            tc_fence_after();
+#pragma unroll 1
+            for (int c = 0; c < kDim / 16; ++c) {
+              uint32_t o[16];
+              tmem_ld_32x32b_x16(to + c * 16, o);
+              tmem_ld_wait_regs(o);
+#pragma unroll
+              for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+              tmem_st_32x32b_x16(to + c * 16, o);
             }
           }
           const float base = m == -INFINITY ? 0.0f : -m;
-          const uint64_t scale2 = pk2(scale, scale), base2 = pk2(base, base);
-          auto weights = [&](auto poly) {
-#pragma unroll
-            for (int c = 0; c < kKeys / 32; ++c) {
-              uint32_t p[16];
-#pragma unroll
-              for (int i = 0; i < 16; ++i) {
-                const uint64_t x =
-                    ffma2_rn(pk2(__uint_as_float(s[c][2 * i]), __uint_as_float(s[c][2 * i + 1])), scale2, base2);
-                uint64_t e;
-                float lo, hi;
-                if (i % 8 >= 8 - decltype(poly)::value) {
-                  e = exp2_poly(x);
-                } else {
-                  upk2(x, lo, hi);
-                  e = pk2(ex2(lo), ex2(hi));
-                }
-                sums[i & 1] = fadd2_rn(sums[i & 1], e);
-                upk2(e, lo, hi);
-                p[i] = pack_bf16(lo, hi);
-              }
-              tmem_st_32x32b_x16(ts + c * 16, p);
-            }
-          };
-          // the polynomial takes neither NaN nor -inf
-          if (kMasked || Sz::kPoly == 0 || __any_sync(0xffffffffu, !(top > -INFINITY)))
-            weights(std::integral_constant<int, 0>{});
-          else
-            weights(std::integral_constant<int, Sz::kPoly>{});
-        };
-        if ((j + 1) * kKeys > all_see)
-          softmax(std::true_type{});
-        else
-          softmax(std::false_type{});
+          weights(0, std::integral_constant<int, 0>{}, scale2, pk2(base, base), sums);
+          weights(1, std::integral_constant<int, 0>{}, scale2, pk2(base, base), sums);
+        }
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bar.p_full[t]);
+        if (lane == 0) mbar_arrive(&bar.p_full[t][buf]);
       }
       if (!ok) break;
+      if (n >= 2) s_phase ^= 1u << (n & 1);   // what stood for the S after the last
       if (n > 0) {
         ok = mbar_wait_soon_warp(&bar.o_full[t], o_phase, a.status, abort);
         if (!ok) break;
@@ -626,6 +630,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int c = 0; c < kDim / 32; ++c) {
         uint32_t o[32];
+        __syncwarp();
         if (n > 0) {
           tmem_ld_32x32b_x32(to + c * 32, o);
           tmem_ld_wait_regs(o);
@@ -656,6 +661,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   if (warp == 8) {
     tc_fence_after();
+    __syncwarp();
     tmem_dealloc(tmem, 512);
   }
 }

@@ -122,10 +122,14 @@ __device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, u
   return ok != 0;
 }
 
-// The same for a converged warp, every lane polling: no lane has to hand the answer on.
+// The same for a whole warp, every lane polling. The lanes may leave the poll at different
+// times: the warp barrier brings them together again for the .aligned instructions that
+// follow such waits.
 __device__ __forceinline__ bool mbar_wait_soon_warp(uint64_t* bar, uint32_t parity, unsigned* status,
                                                     volatile int* abort) {
-  return __all_sync(0xffffffffu, mbar_wait_soon(bar, parity, status, abort));
+  const bool ok = __all_sync(0xffffffffu, mbar_wait_soon(bar, parity, status, abort));
+  __syncwarp();
+  return ok;
 }
 
 // ----------------------------------------------------------------------- TMA
