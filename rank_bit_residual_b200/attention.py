@@ -27,16 +27,18 @@ the page table) are recorded in the status word (svdq_check_status).
 
 from __future__ import annotations
 
-import contextlib
 import ctypes
+import functools
 import math
 from dataclasses import dataclass
 from typing import Optional, Tuple
 
 import torch
 
-from . import (LinearWorkspace, SvdqHeads, SvdqKvCache, SvdqRope, _check, _dt, _ptr, _require_cuda, c_sz,
-               load_library)
+from . import (SVDQ_BF16, SVDQ_F32, LinearWorkspace, SvdqHeads, SvdqKvCache, SvdqRope, _check, c_sz, load_library)
+
+_BF16 = torch.bfloat16
+_TYPES = {torch.bfloat16: SVDQ_BF16, torch.float32: SVDQ_F32}
 
 
 @dataclass
@@ -81,125 +83,158 @@ class Rope:
 
 
 _NO_HEADS = SvdqHeads(None, 0, 0, 0)
+_NO_ROPE = SvdqRope(None, 0, 0, 1.0)
+
+# A decode step calls these functions between kernels of a few microseconds, so their host
+# work counts: what depends on a layout alone is kept by layout (shape, strides, type),
+# pointers go to ctypes as plain ints, and each tensor is asked for a property once.
 
 
-def _on(device):
-    """Work on the tensors' device, whatever the current one is."""
-    if device.index is None or device.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
-    return torch.cuda.device(device)
+def _device(first, *others) -> int:
+    """The index of the one CUDA device that all the tensors live on."""
+    dev = first.get_device()
+    if dev < 0:
+        raise ValueError("tensors must live on a CUDA device")
+    for t in others:
+        if t is not None and t.get_device() != dev:
+            raise ValueError("all tensors must live on one CUDA device")
+    return dev
 
 
-def _same_device(first, **others):
-    _require_cuda(first, *others.values())
-    for name, t in others.items():
-        if t is not None and t.device != first.device:
-            raise ValueError(f"{name} lives on another device")
-    return first.device
+def _raw_stream(dev: int) -> int:
+    """torch.cuda.current_stream(dev).cuda_stream without the stream object (1 us less)."""
+    return torch._C._cuda_getCurrentRawStream(dev)
 
 
-def _strides(t: torch.Tensor):
-    """Strides of all axes but the last; those of axes of one element (which torch leaves
-    free) as a dense tensor has them."""
-    s = [t.stride(i) for i in range(t.dim() - 1)]
-    dense = -(-t.shape[-1] // 8) * 8
-    for i in range(t.dim() - 2, -1, -1):
-        if t.shape[i] <= 1:
-            s[i] = dense
-        dense = max(dense, s[i] * t.shape[i])
-    return s
+def _on_device(call):
+    """Run `call` with the tensors' device current, whatever the caller's current device is
+    (the first argument, a tensor, names it)."""
+    @functools.wraps(call)
+    def run(first, *args, **kwargs):
+        dev = first.get_device()
+        if dev < 0 or dev == torch._C._cuda_getDevice():
+            return call(first, *args, **kwargs)
+        with torch.cuda.device(dev):
+            return call(first, *args, **kwargs)
+    return run
 
 
-def _usable(t: torch.Tensor) -> bool:
-    es = t.element_size()
-    return (t.stride(-1) == 1 or t.shape[-1] == 1) and t.data_ptr() % 16 == 0 and \
-        all(s * es % 16 == 0 and s >= t.shape[-1] for s in _strides(t))
+@functools.lru_cache(maxsize=4096)
+def _layout(shape, stride, size: int):
+    """The strides of all axes but the last, as the library takes them, or None where it
+    cannot: unit stride along the last axis, 16-byte steps along the others, no broadcast.
+    Strides of axes of one element, which torch leaves free, are those of a dense tensor."""
+    dim = shape[-1]
+    if stride[-1] != 1 and dim > 1:
+        return None
+    out = list(stride[:-1])
+    dense = -(-dim // 8) * 8
+    for i in range(len(out) - 1, -1, -1):
+        if shape[i] <= 1:
+            out[i] = dense
+        if out[i] * size % 16 or out[i] < dim:
+            return None
+        dense = max(dense, out[i] * shape[i])
+    return tuple(out)
 
 
-def _check_3d(t, name, dtype, shape=None):
-    if t.dim() != 3:
-        raise ValueError(f"{name} must be [tokens, heads, head_dim]")
+def _heads(t: torch.Tensor, shape):
+    """(descriptor, the tensor it points to) of an input; a copy where the layout needs one."""
+    s, p = _layout(shape, t.stride(), t.element_size()), t.data_ptr()
+    if s is None or p & 15:
+        t = t.clone(memory_format=torch.contiguous_format)
+        s, p = _layout(shape, t.stride(), t.element_size()), t.data_ptr()
+        if s is None:
+            raise ValueError(f"rows of {shape[-1]} elements are not a multiple of 16 bytes")
+    return SvdqHeads(p, s[0], s[1], shape[1]), t
+
+
+def _out_heads(t: Optional[torch.Tensor], name: str, like: torch.Tensor, shape):
+    """(descriptor, tensor) of an output: the given one, or a dense new one."""
+    if t is None:
+        t = like.new_empty(shape)
+    elif t.shape != shape or t.dtype != like.dtype:
+        raise ValueError(f"{name} must be {like.dtype} {tuple(shape)}")
+    s, p = _layout(shape, t.stride(), t.element_size()), t.data_ptr()
+    if s is None or p & 15:
+        raise ValueError(f"{name} needs unit stride along head_dim, 16-byte aligned rows and no broadcast axis")
+    return SvdqHeads(p, s[0], s[1], shape[1]), t
+
+
+def _shape3(t: torch.Tensor, name: str, dtype):
     if t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must be {tuple(shape)}, not {tuple(t.shape)}")
+    shape = t.shape
+    if len(shape) != 3:
+        raise ValueError(f"{name} must be [tokens, heads, head_dim]")
+    return shape
 
 
-def _heads(t: torch.Tensor):
-    """(descriptor, the tensor it points to) of an input; a copy where the layout needs one."""
-    if not _usable(t):
-        t = t.contiguous() if t.data_ptr() % 16 == 0 or not t.is_contiguous() else t.clone()
-    s = _strides(t)
-    return SvdqHeads(t.data_ptr(), s[0], s[1], t.shape[1]), t
-
-
-def _out_heads(t: torch.Tensor, name: str):
-    if not _usable(t):
-        raise ValueError(f"{name} needs unit stride along head_dim, 16-byte aligned rows and no broadcast axis")
-    s = _strides(t)
-    return SvdqHeads(t.data_ptr(), s[0], s[1], t.shape[1])
-
-
-def _vector(t, name, dtype, n):
-    if t is None:
-        return None
-    if t.dtype != dtype or t.dim() != 1 or t.shape[0] != n:
+def _vector(t, name: str, dtype, n: int):
+    if t.dtype != dtype or t.shape != (n,):
         raise ValueError(f"{name} must be {dtype} [{n}]")
-    return t.contiguous()
+    return t if t.is_contiguous() else t.contiguous()
 
 
-def _weights(q_weight, k_weight, dim):
-    given = [w for w in (q_weight, k_weight) if w is not None]
-    for w in given:
-        if tuple(w.shape) != (dim,):
-            raise ValueError(f"a norm weight must be [{dim}]")
-    if len({w.dtype for w in given}) > 1:
-        raise ValueError("the norm weights must have one type")
-    dt = _dt(given[0]) if given else _dt(torch.empty(0, dtype=torch.bfloat16))
+def _ready(w):
+    """A norm weight, contiguous and on a 16-byte boundary."""
+    w = w.contiguous()
+    return w if not w.data_ptr() & 15 else w.clone()
 
-    def ready(w):
+
+def _weights(q_weight, k_weight, dim: int):
+    """(q_weight, k_weight, their pointers, their type) as the library takes them."""
+    dtype = None
+    for w in (q_weight, k_weight):
         if w is None:
-            return None
-        w = w.contiguous()
-        return w if w.data_ptr() % 16 == 0 else w.clone()
-    return ready(q_weight), ready(k_weight), dt
+            continue
+        if w.shape != (dim,):
+            raise ValueError(f"a norm weight must be [{dim}]")
+        if w.dtype not in _TYPES or (dtype is not None and w.dtype != dtype):
+            raise ValueError("the norm weights must have one type, bfloat16 or float32")
+        dtype = w.dtype
+    q_weight = None if q_weight is None else _ready(q_weight)
+    k_weight = None if k_weight is None else _ready(k_weight)
+    return (q_weight, k_weight, None if q_weight is None else q_weight.data_ptr(),
+            None if k_weight is None else k_weight.data_ptr(), SVDQ_BF16 if dtype is None else _TYPES[dtype])
 
 
-def _rope(rope: Optional[Rope], positions, tokens: int, dim: int):
-    """(descriptor, positions, tensors to keep until the launch)."""
-    if rope is None or rope.turns.numel() == 0:
-        return SvdqRope(None, 0, 0, 1.0), None, None
+def _rotation(rope: Optional[Rope], positions, tokens: int, dim: int):
+    """(descriptor, pointer to the positions, tensors to keep until the launch)."""
+    if rope is None:
+        return _NO_ROPE, None, None
+    turns = rope.turns
+    n = turns.numel()
+    if n == 0:
+        return _NO_ROPE, None, None
     if positions is None:
         raise ValueError("a rotation needs positions")
     positions = _vector(positions, "positions", torch.int64, tokens)
-    if rope.turns.dtype != torch.float64 or rope.turns.dim() != 1:
+    if turns.dtype != torch.float64 or turns.dim() != 1:
         raise ValueError("turns must be float64 [rot_dim / 2]")
-    if rope.rot_dim > dim:
+    if 2 * n > dim:
         raise ValueError("rot_dim must not exceed head_dim")
-    turns = rope.turns.contiguous()
-    return SvdqRope(turns.data_ptr(), 2 * turns.numel(), int(bool(rope.interleaved)), float(rope.amplitude)), \
-        positions, turns
+    turns = turns.contiguous()
+    return (SvdqRope(turns.data_ptr(), 2 * n, 1 if rope.interleaved else 0, rope.amplitude), positions.data_ptr(),
+            (positions, turns))
 
 
 def _cache(k_cache, v_cache):
-    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
-        if t.dim() != 4 or t.dtype != torch.bfloat16:
-            raise ValueError(f"{name} must be bfloat16 [pages, page_size, heads, head_dim]")
-    if k_cache.shape != v_cache.shape or _strides(k_cache) != _strides(v_cache):
+    shape, stride = k_cache.shape, k_cache.stride()
+    if len(shape) != 4 or k_cache.dtype != _BF16 or v_cache.dtype != _BF16:
+        raise ValueError("a cache must be bfloat16 [pages, page_size, heads, head_dim]")
+    if v_cache.shape != shape or (v_cache.stride() != stride and _layout(shape, v_cache.stride(), 2) !=
+                                  _layout(shape, stride, 2)):
         raise ValueError("k_cache and v_cache must have one shape and layout")
-    if not _usable(k_cache) or not _usable(v_cache):
-        raise ValueError("a cache needs unit stride along head_dim and 16-byte aligned rows")
-    if k_cache.numel() == 0:
+    if 0 in shape:
         raise ValueError("the cache is empty")
-    pages, page_size, heads, dim = k_cache.shape
-    page_ld, slot_ld, head_ld = _strides(k_cache)
-    return SvdqKvCache(k_cache.data_ptr(), v_cache.data_ptr(), pages, page_ld, slot_ld, head_ld, page_size, heads, dim)
+    s, k, v = _layout(shape, stride, 2), k_cache.data_ptr(), v_cache.data_ptr()
+    if s is None or k & 15 or v & 15:
+        raise ValueError("a cache needs unit stride along head_dim and 16-byte aligned rows")
+    return SvdqKvCache(k, v, shape[0], s[0], s[1], s[2], shape[1], shape[2], shape[3])
 
 
-def _stream_of(device):
-    return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
-
-
+@_on_device
 def svdq_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, positions: Optional[torch.Tensor] = None,
                       rope: Optional[Rope] = None, q_weight: Optional[torch.Tensor] = None,
                       k_weight: Optional[torch.Tensor] = None, eps: float = 1e-6,
@@ -210,33 +245,32 @@ def svdq_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, positions: Optional[torc
     q [T, H, D], k [T, Hkv, D], bf16 or fp32; positions int64 [T]; weights [D] bf16 or
     fp32. q_out=q, k_out=k work in place. Returns (q_out, k_out).
     """
-    lib = load_library()
-    dev = _same_device(q, k=k, positions=positions, q_weight=q_weight, k_weight=k_weight, q_out=q_out, k_out=k_out,
-                       turns=rope.turns if rope is not None else None)
-    _check_3d(q, "q", q.dtype)
-    _check_3d(k, "k", q.dtype, (q.shape[0], k.shape[1] if k.dim() == 3 else 0, q.shape[2]))
-    dt = _dt(q)
-    T, _, D = q.shape
-    if q_out is not None:
-        _check_3d(q_out, "q_out", q.dtype, q.shape)
-    if k_out is not None:
-        _check_3d(k_out, "k_out", q.dtype, k.shape)
-    with _on(dev):
-        qw, kw, wdt = _weights(q_weight, k_weight, D)
-        r, pos, _turns = _rope(rope, positions, T, D)
-        q_out = torch.empty(q.shape, dtype=q.dtype, device=dev) if q_out is None else q_out
-        k_out = torch.empty(k.shape, dtype=k.dtype, device=dev) if k_out is None else k_out
+    dev = _device(q, k, positions, q_weight, k_weight, q_out, k_out, None if rope is None else rope.turns)
+    dt = _TYPES.get(q.dtype)
+    if dt is None:
+        raise ValueError(f"unsupported dtype {q.dtype}")
+    qs, ks = _shape3(q, "q", q.dtype), _shape3(k, "k", q.dtype)
+    T, H, D = qs
+    if ks[0] != T or ks[2] != D:
+        raise ValueError(f"k must be [{T}, heads, {D}]")
+    qw, kw, qw_p, kw_p, wdt = _weights(q_weight, k_weight, D)
+    r, pos, _keep = _rotation(rope, positions, T, D)
+    if T == 0 or H == 0 or ks[1] == 0:   # nothing of q or of k
+        q_out = q.new_empty(qs) if q_out is None else q_out
+        k_out = k.new_empty(ks) if k_out is None else k_out
         if T == 0:
             return q_out, k_out
-        qd, q = _heads(q) if q.shape[1] else (_NO_HEADS, q)
-        kd, k = _heads(k) if k.shape[1] else (_NO_HEADS, k)
-        qo = _out_heads(q_out, "q_out") if q.shape[1] else _NO_HEADS
-        ko = _out_heads(k_out, "k_out") if k.shape[1] else _NO_HEADS
-        _check(lib.svdq_qk_norm_rope(qd, kd, dt, T, D, _ptr(pos), r, _ptr(qw), _ptr(kw), wdt, float(eps), qo, ko,
-                                     _stream_of(dev)), "svdq_qk_norm_rope")
+    qd, q = _heads(q, qs) if H else (_NO_HEADS, q)
+    kd, k = _heads(k, ks) if ks[1] else (_NO_HEADS, k)
+    qo, q_out = _out_heads(q_out, "q_out", q, qs) if H else (_NO_HEADS, q_out)
+    ko, k_out = _out_heads(k_out, "k_out", q, ks) if ks[1] else (_NO_HEADS, k_out)
+    st = load_library().svdq_qk_norm_rope(qd, kd, dt, T, D, pos, r, qw_p, kw_p, wdt, eps, qo, ko, _raw_stream(dev))
+    if st:
+        _check(st, "svdq_qk_norm_rope")
     return q_out, k_out
 
 
+@_on_device
 def svdq_kv_append(k_cache: torch.Tensor, v_cache: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
                    slots: torch.Tensor, positions: Optional[torch.Tensor] = None, rope: Optional[Rope] = None,
                    k_weight: Optional[torch.Tensor] = None, eps: float = 1e-6, q: Optional[torch.Tensor] = None,
@@ -249,46 +283,41 @@ def svdq_kv_append(k_cache: torch.Tensor, v_cache: torch.Tensor, k: torch.Tensor
     twice. q [T, H, D] is normed and rotated in the same pass. k_out receives the
     finished keys too (k_out=k: in place). Returns q_out (None without q).
     """
-    lib = load_library()
-    dev = _same_device(k_cache, v_cache=v_cache, k=k, v=v, slots=slots, positions=positions, k_weight=k_weight, q=q,
-                       q_weight=q_weight, q_out=q_out, k_out=k_out, turns=rope.turns if rope is not None else None)
+    dev = _device(k_cache, v_cache, k, v, slots, positions, k_weight, q, q_weight, q_out, k_out,
+                  None if rope is None else rope.turns)
     c = _cache(k_cache, v_cache)
-    bf16 = torch.bfloat16
-    _check_3d(k, "k", bf16, (k.shape[0], c.heads, c.head_dim))
-    _check_3d(v, "v", bf16, k.shape)
-    T, D = k.shape[0], c.head_dim
+    D = c.head_dim
+    ks, vs = _shape3(k, "k", _BF16), _shape3(v, "v", _BF16)
+    T = ks[0]
+    if ks != (T, c.heads, D) or vs != ks:
+        raise ValueError(f"k and v must be [tokens, {c.heads}, {D}]")
     if q is not None:
-        _check_3d(q, "q", bf16, (T, q.shape[1] if q.dim() == 3 else 0, D))
-        if q.shape[1] == 0:
-            raise ValueError("q has no heads")
-        if q_out is not None:
-            _check_3d(q_out, "q_out", bf16, q.shape)
+        qs = _shape3(q, "q", _BF16)
+        if qs[0] != T or qs[2] != D or qs[1] == 0:
+            raise ValueError(f"q must be [{T}, heads, {D}]")
     elif q_out is not None or q_weight is not None:
         raise ValueError("q_out and q_weight need q")
+    qw, kw, qw_p, kw_p, wdt = _weights(q_weight, k_weight, D)
+    r, pos, _keep = _rotation(rope, positions, T, D)
+    slots = _vector(slots, "slots", torch.int64, T)
+    if T == 0:
+        return q_out if q is None or q_out is not None else q.new_empty(qs)
+    kd, k_in = _heads(k, ks)
+    vd, v = _heads(v, vs)
+    qd = qo = ko = _NO_HEADS
+    if q is not None:
+        qd, q = _heads(q, qs)
+        qo, q_out = _out_heads(q_out, "q_out", q, qs)
     if k_out is not None:
-        _check_3d(k_out, "k_out", bf16, k.shape)
-    with _on(dev):
-        qw, kw, wdt = _weights(q_weight, k_weight, D)
-        r, pos, _turns = _rope(rope, positions, T, D)
-        slots = _vector(slots, "slots", torch.int64, T)
-        if q is not None and q_out is None:
-            q_out = torch.empty(q.shape, dtype=bf16, device=dev)
-        if T == 0:
-            return q_out
-        kd, k = _heads(k)
-        vd, v = _heads(v)
-        qd, q = _heads(q) if q is not None else (_NO_HEADS, None)
-        qo = _out_heads(q_out, "q_out") if q is not None else _NO_HEADS
-        ko = _out_heads(k_out, "k_out") if k_out is not None else _NO_HEADS
-        _check(lib.svdq_kv_append(ctypes.byref(c), kd, vd, _ptr(slots), T, _ptr(pos), r, _ptr(kw), wdt, float(eps),
-                                  qd, _ptr(qw), qo, ko, _stream_of(dev)), "svdq_kv_append")
+        ko, k_out = _out_heads(k_out, "k_out", k, ks)
+    st = load_library().svdq_kv_append(c, kd, vd, slots.data_ptr(), T, pos, r, kw_p, wdt, eps, qd, qw_p, qo, ko,
+                                       _raw_stream(dev))
+    if st:
+        _check(st, "svdq_kv_append")
     return q_out
 
 
-def _scale(scale: Optional[float], dim: int) -> float:
-    return 1.0 / math.sqrt(dim) if scale is None else float(scale)
-
-
+@_on_device
 def svdq_attention_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: Optional[torch.Tensor] = None,
                           cu_k: Optional[torch.Tensor] = None, causal: bool = True,
                           scale: Optional[float] = None, out: Optional[torch.Tensor] = None) -> torch.Tensor:
@@ -300,38 +329,49 @@ def svdq_attention_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_
     sequence are left as they were in `out`, and mean nothing in an output allocated here.
     Returns [Tq, H, D].
     """
-    lib = load_library()
-    dev = _same_device(q, k=k, v=v, cu_q=cu_q, cu_k=cu_k, out=out)
-    bf16 = torch.bfloat16
-    _check_3d(q, "q", bf16)
-    T, H, D = q.shape
-    _check_3d(k, "k", bf16, (k.shape[0], k.shape[1] if k.dim() == 3 else 0, D))
-    _check_3d(v, "v", bf16, k.shape)
-    if H == 0 or k.shape[1] == 0 or H % k.shape[1]:
+    dev = _device(q, k, v, cu_q, cu_k, out)
+    qs, ks, vs = _shape3(q, "q", _BF16), _shape3(k, "k", _BF16), _shape3(v, "v", _BF16)
+    T, H, D = qs
+    if ks[2] != D or vs != ks:
+        raise ValueError(f"k and v must be of one size [keys, heads, {D}]")
+    if H == 0 or ks[1] == 0 or H % ks[1]:
         raise ValueError("the query heads must be a multiple of the key heads")
+    batch = -1
     for name, cu in (("cu_q", cu_q), ("cu_k", cu_k)):
-        if cu is not None and (cu.dtype != torch.int32 or cu.dim() != 1 or cu.shape[0] < 1):
-            raise ValueError(f"{name} must be int32 [batch + 1]")
-    sizes = [cu.shape[0] - 1 if cu is not None else 1 for cu in (cu_q, cu_k)]
-    if sizes[0] != sizes[1]:
-        raise ValueError("cu_q and cu_k must have one length")
-    if out is not None:
-        _check_3d(out, "out", bf16, q.shape)
-    with _on(dev):
-        out = torch.empty(q.shape, dtype=bf16, device=dev) if out is None else out
-        if T == 0:
-            return out
-        qd, q = _heads(q)
-        kd, k = _heads(k)
-        vd, v = _heads(v)
-        cu_q = cu_q.contiguous() if cu_q is not None else None
-        cu_k = cu_k.contiguous() if cu_k is not None else None
-        _check(lib.svdq_attention_prompt(qd, kd, vd, _ptr(cu_q), _ptr(cu_k), sizes[0], T, k.shape[0], D,
-                                         int(bool(causal)), _scale(scale, D), _out_heads(out, "out"), _stream_of(dev)),
-               "svdq_attention_prompt")
+        n = 1
+        if cu is not None:
+            if cu.dtype != torch.int32 or cu.dim() != 1 or cu.numel() < 1:
+                raise ValueError(f"{name} must be int32 [batch + 1]")
+            n = cu.numel() - 1
+        if batch not in (-1, n):
+            raise ValueError("cu_q and cu_k must have one length")
+        batch = n
+    scale = 1.0 / math.sqrt(D) if scale is None else float(scale)
+    qo, out = _out_heads(out, "out", q, qs)
+    if T == 0:
+        return out
+    qd, q = _heads(q, qs)
+    kd, k = _heads(k, ks)
+    vd, v = _heads(v, vs)
+    cu_q = None if cu_q is None else cu_q.contiguous()
+    cu_k = None if cu_k is None else cu_k.contiguous()
+    st = load_library().svdq_attention_prompt(
+        qd, kd, vd, None if cu_q is None else cu_q.data_ptr(), None if cu_k is None else cu_k.data_ptr(), batch, T,
+        ks[0], D, 1 if causal else 0, scale, qo, _raw_stream(dev))
+    if st:
+        _check(st, "svdq_attention_prompt")
     return out
 
 
+@functools.lru_cache(maxsize=4096)
+def _decode_scratch(dev: int, batch: int, heads: int, kv_heads: int, dim: int) -> int:
+    size = c_sz()
+    _check(load_library().svdq_attention_decode_workspace_size(batch, heads, kv_heads, dim, ctypes.byref(size)),
+           "svdq_attention_decode_workspace_size")
+    return size.value
+
+
+@_on_device
 def svdq_attention_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, page_table: torch.Tensor,
                           kv_len: torch.Tensor, scale: Optional[float] = None, out: Optional[torch.Tensor] = None,
                           workspace: Optional[LinearWorkspace] = None) -> torch.Tensor:
@@ -341,32 +381,29 @@ def svdq_attention_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch
     [B] (0: a zero row). The scratch is allocated per call unless a workspace is given
     (one per stream in flight). Returns [B, H, D].
     """
-    lib = load_library()
-    dev = _same_device(q, k_cache=k_cache, v_cache=v_cache, page_table=page_table, kv_len=kv_len, out=out)
-    bf16 = torch.bfloat16
+    dev = _device(q, k_cache, v_cache, page_table, kv_len, out)
     c = _cache(k_cache, v_cache)
-    _check_3d(q, "q", bf16, (q.shape[0], q.shape[1] if q.dim() == 3 else 0, c.head_dim))
-    B, H, D = q.shape
+    qs = _shape3(q, "q", _BF16)
+    B, H, D = qs
+    if D != c.head_dim:
+        raise ValueError(f"q must be [batch, heads, {c.head_dim}]")
     if H == 0 or H % c.heads:
         raise ValueError("the query heads must be a multiple of the key heads")
     if page_table.dtype != torch.int32 or page_table.dim() != 2 or page_table.shape[0] != B:
         raise ValueError(f"page_table must be int32 [{B}, pages]")
     kv_len = _vector(kv_len, "kv_len", torch.int32, B)
-    if out is not None:
-        _check_3d(out, "out", bf16, q.shape)
-    with _on(dev):
-        out = torch.empty(q.shape, dtype=bf16, device=dev) if out is None else out
-        if B == 0:
-            return out
-        page_table = page_table.contiguous()
-        size = c_sz()
-        _check(lib.svdq_attention_decode_workspace_size(B, H, c.heads, D, ctypes.byref(size)), "workspace")
-        ws = workspace.get(size.value, dev) if workspace is not None else \
-            torch.empty(size.value, dtype=torch.uint8, device=dev)
-        qd, q = _heads(q)
-        _check(lib.svdq_attention_decode(qd, ctypes.byref(c), _ptr(page_table), page_table.shape[1], _ptr(kv_len), B,
-                                         _scale(scale, D), _out_heads(out, "out"), _ptr(ws), ws.numel(),
-                                         _stream_of(dev)), "svdq_attention_decode")
+    scale = 1.0 / math.sqrt(D) if scale is None else float(scale)
+    qo, out = _out_heads(out, "out", q, qs)
+    if B == 0:
+        return out
+    page_table = page_table.contiguous()
+    size = _decode_scratch(dev, B, H, c.heads, D)
+    ws = q.new_empty(size, dtype=torch.uint8) if workspace is None else workspace.get(size, q.device)
+    qd, q = _heads(q, qs)
+    st = load_library().svdq_attention_decode(qd, c, page_table.data_ptr(), page_table.shape[1], kv_len.data_ptr(), B,
+                                              scale, qo, ws.data_ptr(), ws.numel(), _raw_stream(dev))
+    if st:
+        _check(st, "svdq_attention_decode")
     return out
 
 
