@@ -4,20 +4,20 @@
 //   y = x * rsqrt(mean(x^2) + eps) * w,   then per pair  A (a cos - b sin, b cos + a sin)
 //
 // Every row is read once and written once; nothing else moves, so the pass is bound by
-// HBM (a few tokens: by the latency of one load, one reduction and one store). A group of
-// 8, 16 or 32 lanes (head_dim up to 64, 128, 256) holds a row, eight consecutive
-// elements per lane (16-byte loads of bf16). A warp takes a token, or a share of its heads:
-// the cosines are the same for all heads, so its lanes compute them once, and each lane
-// keeps what it needs of them in registers while the rows go by, the next ones in flight behind these:
+// HBM, if it issues few enough instructions (a few tokens: by the latency of one load, one
+// reduction and one store). A group of 4, 8 or 16 lanes (head_dim up to 64, 128, 256)
+// holds a row, each lane two chunks of eight consecutive elements (16-byte loads of bf16).
+// In the half layout a lane's two chunks are partners when rot_dim / 2 is a multiple of 8,
+// so that a rotation needs no exchange:
 //   y_i = inv (x_i A_i + x_partner B_i),   A = w cos,   B = -+ w_partner sin
-// The partner of an element in the half layout sits in another lane at the same place
-// (exchanged as it lies in memory, two bf16 per shuffle) when rot_dim / 2 is a multiple
-// of 8, else the row goes through shared memory. Angles are exact to 2^-32 of a turn at
-// any position: a frequency is a 64-bit fraction of a turn, and its integer product with
-// the position wraps at whole turns by itself. (fp64 products cost more than the rows of
-// two heads: 69 -> 47 us for 8192 tokens came from halving their number.) Warps wait for nothing but their own loads;
-// with blocks of four tokens that shared their cosines behind a barrier, that start of every
-// block took as long as its rows.
+// and the norm three shuffles for four rows of 128. (With one chunk per lane: 150
+// instructions for two rows of 128 elements, 47 us for 8192 tokens of 40 heads.) Other
+// half layouts pass the row through shared memory. A warp takes a token, or a share of its heads:
+// the cosines are the same for all heads, so its lanes compute them once, and each lane
+// keeps what it needs of them in registers while the rows go by, the next ones in flight
+// behind these. Angles are exact to 2^-32 of a turn at any position: a frequency is
+// a 64-bit fraction of a turn, and its integer product with the position wraps at whole
+// turns by itself. Warps wait for nothing but their own loads.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -32,14 +32,13 @@ namespace svdq {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kVec = 8;           // elements per lane
+constexpr int kVec = 8;           // elements of a chunk; a lane has two
 constexpr int kWarps = kThreads / 32;
-constexpr int kBlocksPerSm = 3;
+constexpr int kBlocksPerSm = 2;
 constexpr int kMaxDim = 256;
-constexpr int kFlight = 2;        // rows of a group that are loaded together, one such set ahead
 
 // How the partner of a rotated element is found.
-enum Pairing { kShuffle = 0, kNeighbour = 1, kThroughShared = 2 };
+enum Pairing { kHalves = 0, kNeighbour = 1, kThroughShared = 2 };
 
 // Eight elements as they lie in memory.
 template <typename T>
@@ -98,18 +97,72 @@ __device__ __forceinline__ void take8(const float* p, float (&x)[kVec]) {
 template <typename T, int kLanes, int kPairing>
 __global__ void __launch_bounds__(kThreads, kBlocksPerSm) heads_kernel(const __grid_constant__ HeadsArgs a, const int shares) {
   constexpr int kGroups = 32 / kLanes;   // rows of a warp at a time
+  // sets of rows that are loaded together, one set ahead: as many as the registers hold
+  // (two sets of bf16 rows: 41 -> 37 us for 8192 tokens of 40 heads)
+  constexpr int kFlight = sizeof(T) == 2 ? 2 : 1;
   __shared__ __align__(16) float sh_w[2][kMaxDim];
   __shared__ unsigned long long sh_turns[kMaxDim / 2];   // in 2^-64 of a turn
   __shared__ __align__(16) float sh_cos[kWarps][kMaxDim / 2], sh_sin[kWarps][kMaxDim / 2];
-  __shared__ __align__(16) T sh_row[kPairing == kThroughShared ? kThreads * kVec : 1];
+  __shared__ __align__(16) T sh_row[kPairing == kThroughShared ? kThreads * 2 * kVec : 1];
 
   const int warp = threadIdx.x / 32;
   const int lane = threadIdx.x % kLanes;                 // in the row
   const int group = threadIdx.x % 32 / kLanes;
   const int half = a.rope.rot_dim / 2;
-  const int e0 = lane * kVec;
-  const bool in_row = e0 < a.head_dim;
   const float inv_dim = 1.0f / static_cast<float>(a.head_dim);
+
+  // the two chunks of this lane, by their first element
+  int e[2] = {2 * lane * kVec, (2 * lane + 1) * kVec};
+  const bool partners = kPairing == kHalves && lane < half / kVec;   // the two are each other's
+  if (partners) e[0] = lane * kVec, e[1] = lane * kVec + half;
+  const bool on[2] = {e[0] < a.head_dim, e[1] < a.head_dim};
+
+  const unsigned units = static_cast<unsigned>(a.tokens) * shares;   // below 2^31
+  const unsigned warps = gridDim.x * kWarps;
+  const int stride = kGroups * shares;
+
+  // what a unit needs first is loaded while the one before it is worked on
+  int64_t next_position = 0, next_slot = -1;
+  auto look_ahead = [&](unsigned unit) {
+    if (unit >= units) return;
+    const unsigned t = shares == 1 ? unit : unit / shares;
+    if (half > 0) next_position = a.positions[t];
+    if (a.cache.k) next_slot = a.slots[t];
+  };
+  Raw<T> now[kFlight][2], next[kFlight][2];
+#pragma unroll
+  for (int u = 0; u < kFlight; ++u)   // chunks past head_dim stay zero
+#pragma unroll
+    for (int c = 0; c < 2; ++c) now[u][c].zero(), next[u][c].zero();
+
+  unsigned unit = blockIdx.x * kWarps + warp;
+  int64_t t = 0;
+  int share = 0, h0 = 0;   // heads h0, h0 + stride, ... are this group's
+  // The rows of this group in one tensor, a set of kFlight at a time, the next set in
+  // flight. start() loads the first set; every lane makes the same number of turns.
+  auto load_set = [&](const svdq_heads& src, Raw<T> (&set)[kFlight][2], const T*& p, int first) {
+    const int64_t step = stride * src.head_ld;
+#pragma unroll
+    for (int u = 0; u < kFlight; ++u, p += step)
+      if (first + u * stride + h0 < src.heads) {
+        if (on[0]) set[u][0].load(p + e[0]);
+        if (on[1]) set[u][1].load(p + e[1]);
+      }
+  };
+  auto start = [&](const svdq_heads& src) {
+    const T* p = static_cast<const T*>(src.data) + t * src.token_ld + h0 * src.head_ld;
+    load_set(src, now, p, 0);
+    return p;
+  };
+  auto start_unit = [&]() -> const T* {
+    if (unit >= units) return nullptr;
+    t = shares == 1 ? unit : unit / shares;
+    share = static_cast<int>(unit - static_cast<unsigned>(t) * shares);
+    h0 = share * kGroups + group;
+    return start(a.q.heads > 0 ? a.q : a.k);
+  };
+  look_ahead(unit);
+  const T* from = start_unit();
 
   for (int i = threadIdx.x; i < a.head_dim; i += kThreads) {
 #pragma unroll
@@ -126,67 +179,28 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) heads_kernel(const __g
   }
   __syncthreads();
 
-  // the partner of element e of a head, and its lane here
-  auto partner_of = [&](int e) {
-    if (e >= a.rope.rot_dim) return e;
-    return kPairing == kNeighbour ? e ^ 1 : (e < half ? e + half : e - half);
-  };
-  const int partner = partner_of(e0) / kVec;
-  const unsigned units = static_cast<unsigned>(a.tokens) * shares;   // below 2^31
-  const unsigned warps = gridDim.x * kWarps;
-  const int stride = kGroups * shares;
-
-  // what a unit needs first is loaded while the one before it is worked on
-  int64_t next_position = 0, next_slot = -1;
-  auto look_ahead = [&](unsigned unit) {
-    if (unit >= units) return;
-    const unsigned t = shares == 1 ? unit : unit / shares;
-    if (half > 0) next_position = a.positions[t];
-    if (a.cache.k) next_slot = a.slots[t];
-  };
-  Raw<T> now[kFlight], next[kFlight];
-#pragma unroll
-  for (int u = 0; u < kFlight; ++u) now[u].zero(), next[u].zero();   // lanes past head_dim stay so
-
-  unsigned unit = blockIdx.x * kWarps + warp;
-  look_ahead(unit);
-  for (; unit < units; unit += warps) {
-    const int64_t t = shares == 1 ? unit : unit / shares;
-    const int share = static_cast<int>(unit - static_cast<unsigned>(t) * shares);
-    const int h0 = share * kGroups + group;   // heads h0, h0 + stride, ... are this group's
+  while (unit < units) {
     const int64_t position_now = next_position, slot = next_slot;
     look_ahead(unit + warps);
-
-    // The rows of this group in one tensor, a set of kFlight at a time, the next set in
-    // flight. start() loads the first set; every lane makes the same number of turns.
-    auto load_set = [&](const svdq_heads& src, Raw<T> (&set)[kFlight], const T*& p, int first) {
-      const int64_t step = stride * src.head_ld;
-      const int left = in_row ? src.heads - h0 : 0;
-#pragma unroll
-      for (int u = 0; u < kFlight; ++u, p += step)
-        if (first + u * stride < left) set[u].load(p);
-    };
-    auto start = [&](const svdq_heads& src) {
-      const T* p = static_cast<const T*>(src.data) + t * src.token_ld + h0 * src.head_ld + e0;
-      load_set(src, now, p, 0);
-      return p;
-    };
     auto walk = [&](const svdq_heads& src, const T* p, auto&& use) {
-      const int left = in_row ? src.heads - h0 : 0;
       for (int first = 0; first < src.heads; first += kFlight * stride) {
         load_set(src, next, p, first + kFlight * stride);
 #pragma unroll
         for (int u = 0; u < kFlight; ++u) {
-          if (first + u * stride < src.heads) use(now[u], first + u * stride < left);
-          now[u] = next[u];
+          if (first + u * stride < src.heads) use(now[u], first + u * stride + h0 < src.heads);
+          now[u][0] = next[u][0];
+          now[u][1] = next[u][1];
         }
       }
     };
     // a running pointer to where rows go
     auto row_of = [&](void* data, int64_t token_row, int64_t head_ld) {
-      return static_cast<T*>(data) + token_row + h0 * head_ld + e0;
+      return static_cast<T*>(data) + token_row + h0 * head_ld;
     };
-    const T* from = start(a.q.heads > 0 ? a.q : a.k);
+    auto put_row = [&](T* p, const Raw<T> (&y)[2]) {
+      if (on[0]) y[0].store(p + e[0]);
+      if (on[1]) y[1].store(p + e[1]);
+    };
 
     // where the token's key and value go in the cache
     int64_t cache_row = -1;
@@ -201,6 +215,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) heads_kernel(const __g
         cache_row = page * a.cache.page_ld + (slot - page * a.cache.page_size) * a.cache.slot_ld;
       }
     }
+
     if (half > 0) {
       const unsigned long long position = static_cast<unsigned long long>(position_now);
       for (int j = threadIdx.x % 32; j < half; j += 32) {
@@ -214,64 +229,74 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) heads_kernel(const __g
       __syncwarp();
     }
 
+    // the partner of an element that turns, and its pair
+    auto partner_of = [&](int i) { return kPairing == kNeighbour ? i ^ 1 : (i < half ? i + half : i - half); };
+    auto pair_of = [&](int i) { return kPairing == kNeighbour ? i >> 1 : (i < half ? i : i - half); };
+
     auto turn_heads = [&](const svdq_heads& src, const T* p, const void* weight, const float* w, auto&& store) {
-      uint64_t own[kVec / 2], theirs[kVec / 2];   // A and B
-      uint32_t mask[Raw<T>::kWords];              // 0 where no partner takes part
-      // eight consecutive floats, or those of the pairs of eight consecutive elements
-      float we[kVec], wp[kVec], co[kVec], si[kVec];
-      const bool turns0 = e0 < a.rope.rot_dim;
-      const int ew = in_row ? e0 : 0;
-      take8(w + ew, we);
-      if (kPairing == kNeighbour) {
+      uint64_t own[2][kVec / 2], theirs[2][kVec / 2];   // A and B
+      uint32_t mask[2][Raw<T>::kWords];                 // 0 where no partner takes part
+      {
+        float we[2][kVec];
 #pragma unroll
-        for (int i = 0; i < kVec; i += 2) {
-          wp[i] = we[i + 1], wp[i + 1] = we[i];
-          const int j = e0 + i < a.rope.rot_dim ? (e0 + i) >> 1 : 0;
-          co[i] = co[i + 1] = sh_cos[warp][j];
-          si[i + 1] = sh_sin[warp][j];
-          si[i] = -si[i + 1];
-        }
-      } else if (kPairing == kShuffle) {   // all eight turn, or none
-        const int j = turns0 ? (e0 < half ? e0 : e0 - half) : 0;
-        take8(w + (turns0 ? partner * kVec : 0), wp);
-        take8(sh_cos[warp] + j, co);
-        take8(sh_sin[warp] + j, si);
-        if (e0 < half) {
+        for (int c = 0; c < 2; ++c) take8(w + (on[c] ? e[c] : 0), we[c]);
+        if (kPairing == kHalves) {
+          float co[kVec], si[kVec];
+          take8(sh_cos[warp] + (partners ? e[0] : 0), co);
+          take8(sh_sin[warp] + (partners ? e[0] : 0), si);
 #pragma unroll
-          for (int i = 0; i < kVec; ++i) si[i] = -si[i];
-        }
-      } else {
+          for (int i = 0; i < kVec; ++i) {
+            if (!partners) co[i] = 1.0f, si[i] = 0.0f;
+          }
 #pragma unroll
-        for (int i = 0; i < kVec; ++i) {
-          const int e = e0 + i, j = e < half ? e : e - half;
-          const bool turns = e < a.rope.rot_dim;
-          wp[i] = w[turns ? partner_of(e) : 0];
-          co[i] = sh_cos[warp][turns ? j : 0];
-          si[i] = sh_sin[warp][turns ? j : 0];
-          if (e < half) si[i] = -si[i];
+          for (int i = 0; i < kVec; i += 2) {
+            own[0][i / 2] = pk2(we[0][i] * co[i], we[0][i + 1] * co[i + 1]);
+            own[1][i / 2] = pk2(we[1][i] * co[i], we[1][i + 1] * co[i + 1]);
+            theirs[0][i / 2] = pk2(-we[1][i] * si[i], -we[1][i + 1] * si[i + 1]);
+            theirs[1][i / 2] = pk2(we[0][i] * si[i], we[0][i + 1] * si[i + 1]);
+          }
+#pragma unroll
+          for (int i = 0; i < Raw<T>::kWords; ++i) mask[0][i] = mask[1][i] = partners ? 0xFFFFFFFFu : 0u;
+        } else {
+#pragma unroll
+          for (int c = 0; c < 2; ++c)
+#pragma unroll
+            for (int i = 0; i < kVec; i += 2) {
+              // rot_dim is even: both of two consecutive elements turn, or neither
+              const bool turns = e[c] + i < a.rope.rot_dim;
+              float own2[2] = {we[c][i], we[c][i + 1]}, theirs2[2] = {0.0f, 0.0f};
+              if (turns) {
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+                  const int el = e[c] + i + b, j = pair_of(el);
+                  const bool first = kPairing == kNeighbour ? b == 0 : el < half;
+                  const float si = sh_sin[warp][j];
+                  own2[b] *= sh_cos[warp][j];
+                  theirs2[b] = w[partner_of(el)] * (first ? -si : si);
+                }
+              }
+              own[c][i / 2] = pk2(own2[0], own2[1]);
+              theirs[c][i / 2] = pk2(theirs2[0], theirs2[1]);
+              if (sizeof(T) == 2)
+                mask[c][i / 2] = turns ? 0xFFFFFFFFu : 0u;
+              else
+                mask[c][i % Raw<T>::kWords] = mask[c][(i + 1) % Raw<T>::kWords] = turns ? 0xFFFFFFFFu : 0u;
+            }
         }
       }
-#pragma unroll
-      for (int i = 0; i < kVec; i += 2) {
-        // rot_dim is even: both of two consecutive elements turn, or neither
-        const bool turns = e0 + i < a.rope.rot_dim;
-        own[i / 2] = turns ? pk2(we[i] * co[i], we[i + 1] * co[i + 1]) : pk2(we[i], we[i + 1]);
-        theirs[i / 2] = turns ? pk2(wp[i] * si[i], wp[i + 1] * si[i + 1]) : 0;
-        if (sizeof(T) == 2)
-          mask[i / 2] = turns ? 0xFFFFFFFFu : 0u;
-        else
-          mask[i % Raw<T>::kWords] = mask[(i + 1) % Raw<T>::kWords] = turns ? 0xFFFFFFFFu : 0u;
-      }
-      walk(src, p, [&](Raw<T>& raw, bool live) {
-        uint64_t x[kVec / 2];
-        raw.get(x);
+      walk(src, p, [&](Raw<T> (&raw)[2], bool live) {
+        uint64_t x[2][kVec / 2];
+        raw[0].get(x[0]);
+        raw[1].get(x[1]);
         uint64_t inv2 = pk2(1.0f, 1.0f);
         if (weight) {
-          uint64_t s2 = fmul2_rn(x[0], x[0]);
+          uint64_t s2[2] = {fmul2_rn(x[0][0], x[0][0]), fmul2_rn(x[1][0], x[1][0])};
 #pragma unroll
-          for (int i = 1; i < kVec / 2; ++i) s2 = ffma2_rn(x[i], x[i], s2);
+          for (int i = 1; i < kVec / 2; ++i)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) s2[c] = ffma2_rn(x[c][i], x[c][i], s2[c]);
           float ss, s1;
-          upk2(s2, ss, s1);
+          upk2(fadd2_rn(s2[0], s2[1]), ss, s1);
           ss += s1;
 #pragma unroll
           for (int o = kLanes / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
@@ -279,44 +304,66 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) heads_kernel(const __g
           inv2 = pk2(inv, inv);
         }
         if (half > 0) {
-          Raw<T> raw2;
-          if (kPairing == kNeighbour) {
+          uint64_t y[2][kVec / 2];
+          const bool partial = 2 * half < a.head_dim;   // then some values take no part, and must
+                                                        // not meet B = 0 as infinities
+          Raw<T> other[2];
+          if (kPairing == kHalves) {
+            other[0] = raw[1], other[1] = raw[0];
+          } else if (kPairing == kNeighbour) {
 #pragma unroll
-            for (int i = 0; i < Raw<T>::kWords; ++i)
-              raw2.w[i] = sizeof(T) == 2 ? __byte_perm(raw.w[i], 0, 0x1032) : raw.w[(i ^ 1) % Raw<T>::kWords];
-          } else if (kPairing == kShuffle) {
+            for (int c = 0; c < 2; ++c)
 #pragma unroll
-            for (int i = 0; i < Raw<T>::kWords; ++i) raw2.w[i] = __shfl_sync(0xffffffffu, raw.w[i], partner, kLanes);
+              for (int i = 0; i < Raw<T>::kWords; ++i)
+                other[c].w[i] =
+                    sizeof(T) == 2 ? __byte_perm(raw[c].w[i], 0, 0x1032) : raw[c].w[(i ^ 1) % Raw<T>::kWords];
           } else {
-            T* row = sh_row + (kPairing == kThroughShared ? (threadIdx.x - lane) * kVec : 0);
-            raw.store(row + e0);
-            __syncwarp();
-            T mine[kVec];
-#pragma unroll
-            for (int i = 0; i < kVec; ++i) mine[i] = row[partner_of(e0 + i)];
+            T* row = sh_row + (kPairing == kThroughShared ? (threadIdx.x - lane) * 2 * kVec : 0);
+            raw[0].store(row + e[0]);
+            raw[1].store(row + e[1]);
             __syncwarp();
 #pragma unroll
-            for (int i = 0; i < Raw<T>::kWords; ++i) raw2.w[i] = reinterpret_cast<const uint32_t*>(mine)[i];
-          }
-          if (2 * half < a.head_dim) {
-            // a value that takes no part must not meet B = 0 as an infinity
+            for (int c = 0; c < 2; ++c) {
+              T mine[kVec];
 #pragma unroll
-            for (int i = 0; i < Raw<T>::kWords; ++i) raw2.w[i] &= mask[i];
-          }
-          uint64_t y[kVec / 2];
-          raw2.get(y);
+              for (int i = 0; i < kVec; ++i) mine[i] = row[e[c] + i < a.rope.rot_dim ? partner_of(e[c] + i) : 0];
 #pragma unroll
-          for (int i = 0; i < kVec / 2; ++i) x[i] = ffma2_rn(y[i], theirs[i], fmul2_rn(x[i], own[i]));
+              for (int i = 0; i < Raw<T>::kWords; ++i) other[c].w[i] = reinterpret_cast<const uint32_t*>(mine)[i];
+            }
+            __syncwarp();
+          }
+          if (kPairing == kHalves && !partial) {
+#pragma unroll
+            for (int i = 0; i < kVec / 2; ++i) y[0][i] = x[1][i], y[1][i] = x[0][i];
+          } else {
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              if (partial) {
+#pragma unroll
+                for (int i = 0; i < Raw<T>::kWords; ++i) other[c].w[i] &= mask[c][i];
+              }
+              other[c].get(y[c]);
+            }
+          }
+#pragma unroll
+          for (int c = 0; c < 2; ++c)
+#pragma unroll
+            for (int i = 0; i < kVec / 2; ++i) x[c][i] = ffma2_rn(y[c][i], theirs[c][i], fmul2_rn(x[c][i], own[c][i]));
         } else {
 #pragma unroll
-          for (int i = 0; i < kVec / 2; ++i) x[i] = fmul2_rn(x[i], own[i]);
+          for (int c = 0; c < 2; ++c)
+#pragma unroll
+            for (int i = 0; i < kVec / 2; ++i) x[c][i] = fmul2_rn(x[c][i], own[c][i]);
         }
         if (weight) {
 #pragma unroll
-          for (int i = 0; i < kVec / 2; ++i) x[i] = fmul2_rn(x[i], inv2);
+          for (int c = 0; c < 2; ++c)
+#pragma unroll
+            for (int i = 0; i < kVec / 2; ++i) x[c][i] = fmul2_rn(x[c][i], inv2);
         }
-        Raw<T> out;
-        out.put(x);
+        Raw<T> out[2];
+        out[0].put(x[0]);
+        out[1].put(x[1]);
         store(out, live);
       });
     };
@@ -324,8 +371,8 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) heads_kernel(const __g
     if (a.q.heads > 0) {
       T* q = row_of(a.q_out.data, t * a.q_out.token_ld, a.q_out.head_ld);
       const int64_t step = stride * a.q_out.head_ld;
-      turn_heads(a.q, from, a.q_weight, sh_w[0], [&](const Raw<T>& y, bool live) {
-        if (live) y.store(q);
+      turn_heads(a.q, from, a.q_weight, sh_w[0], [&](const Raw<T> (&y)[2], bool live) {
+        if (live) put_row(q, y);
         q += step;
       });
       from = start(a.k);
@@ -334,21 +381,23 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) heads_kernel(const __g
       T* k = a.k_out.data ? row_of(a.k_out.data, t * a.k_out.token_ld, a.k_out.head_ld) : nullptr;
       T* c = cache_row >= 0 ? row_of(a.cache.k, cache_row, a.cache.head_ld) : nullptr;
       const int64_t step = stride * a.k_out.head_ld, c_step = stride * a.cache.head_ld;
-      turn_heads(a.k, from, a.k_weight, sh_w[1], [&](const Raw<T>& y, bool live) {
-        if (live && a.k_out.data) y.store(k);
-        if (live && cache_row >= 0) y.store(c);
+      turn_heads(a.k, from, a.k_weight, sh_w[1], [&](const Raw<T> (&y)[2], bool live) {
+        if (live && a.k_out.data) put_row(k, y);
+        if (live && cache_row >= 0) put_row(c, y);
         k += step, c += c_step;
       });
     }
     if (a.cache.k) {
       T* c = cache_row >= 0 ? row_of(a.cache.v, cache_row, a.cache.head_ld) : nullptr;
       const int64_t c_step = stride * a.cache.head_ld;
-      walk(a.v, start(a.v), [&](const Raw<T>& y, bool live) {
-        if (live && cache_row >= 0) y.store(c);
+      walk(a.v, start(a.v), [&](const Raw<T> (&y)[2], bool live) {
+        if (live && cache_row >= 0) put_row(c, y);
         c += c_step;
       });
     }
     __syncwarp();   // the cosines may be written again
+    unit += warps;
+    from = start_unit();
   }
 }
 
@@ -368,15 +417,15 @@ cudaError_t launch_pairing(const HeadsArgs& a, cudaStream_t st) {
 template <typename T, int kLanes>
 cudaError_t launch_lanes(const HeadsArgs& a, cudaStream_t st) {
   if (a.rope.interleaved) return launch_pairing<T, kLanes, kNeighbour>(a, st);
-  if (a.rope.rot_dim / 2 % kVec == 0) return launch_pairing<T, kLanes, kShuffle>(a, st);
+  if (a.rope.rot_dim / 2 % kVec == 0) return launch_pairing<T, kLanes, kHalves>(a, st);
   return launch_pairing<T, kLanes, kThroughShared>(a, st);
 }
 
 template <typename T>
 cudaError_t launch_type(const HeadsArgs& a, cudaStream_t st) {
-  if (a.head_dim <= 64) return launch_lanes<T, 8>(a, st);
-  if (a.head_dim <= 128) return launch_lanes<T, 16>(a, st);
-  return launch_lanes<T, 32>(a, st);
+  if (a.head_dim <= 64) return launch_lanes<T, 4>(a, st);
+  if (a.head_dim <= 128) return launch_lanes<T, 8>(a, st);
+  return launch_lanes<T, 16>(a, st);
 }
 
 }  // namespace
