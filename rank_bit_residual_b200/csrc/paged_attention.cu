@@ -7,7 +7,9 @@
 // head of a group, so HBM bounds it. The work is cut without regard to heads and
 // sequences: the keys of all (sequence, key head) segments, in units of 16, form one
 // line that is dealt evenly to two blocks per SM, so that ragged batches and single long
-// sequences both fill the GPU. Inside a block four warps take a piece's units in turn,
+// sequences both fill the GPU. Up to eight segments of a sequence share the line, each with a
+// block of its own per range: blocks that run side by side then read rows of the same
+// tokens, which lie side by side. Inside a block four warps take a piece's units in turn,
 // each with its own ring of asynchronous copies and its own running softmax, without any
 // barrier until the piece ends.
 //
@@ -38,6 +40,7 @@ constexpr int kThreads = kWarps * 32;
 constexpr int kUnit = 16;          // keys per unit of work
 constexpr int kBlocksPerSm = 2;
 constexpr int kRow = 8;            // heads per column tile of the products
+constexpr int kMaxRanges = 512;    // of the line: at most kBlocksPerSm per SM
 
 struct PagedArgs {
   svdq_heads q, out;
@@ -51,7 +54,8 @@ struct PagedArgs {
   float scale_log2; // scale * log2(e)
   float* scratch;
   unsigned* status;
-  int grid;         // blocks of the first kernel
+  int abreast;      // segments of a sequence that share the line: 8, 4, 2 or 1
+  int grid;         // ranges of the line at most: blocks of the first kernel / abreast
 };
 
 // Floats of one partial result: sums [rows][kDim], then maxima and totals [rows].
@@ -95,7 +99,7 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-// Blocks that share `total` units: no block has less than a unit for each warp unless
+// Ranges that share `total` units: none has less than a unit for each warp unless
 // there is no more than that altogether. 0 without any unit.
 __device__ __forceinline__ int blocks_for(long long total, int grid) {
   return static_cast<int>(min(static_cast<long long>(grid), (total + kWarps - 1) / kWarps));
@@ -134,7 +138,8 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) paged_split_kernel(con
   pdl_trigger();
 
   // this block's range [lo, hi) of the line of units, and the sequence it begins in
-  const int segs = a.cache.heads * a.row_groups;   // segments per sequence
+  const int segs = a.cache.heads * a.row_groups / a.abreast;   // of the line, per sequence
+  const int range = blockIdx.x / a.abreast, beside = blockIdx.x - range * a.abreast;
   long long mine = 0;
   for (int s = tid; s < a.batch; s += kThreads) {
     const int len = clamped_len(a, s);
@@ -143,8 +148,8 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) paged_split_kernel(con
   }
   const long long total = block_sum(mine, sh_sum) * segs;
   const int blocks = blocks_for(total, a.grid);
-  if (blockIdx.x >= blocks) return;
-  const long long lo = total * blockIdx.x / blocks, hi = total * (blockIdx.x + 1) / blocks;
+  if (range >= blocks) return;
+  const long long lo = total * range / blocks, hi = total * (range + 1) / blocks;
   long long before = 0;
   for (int s0 = 0; s0 < a.batch; s0 += kThreads) {
     __syncthreads();
@@ -191,8 +196,9 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) paged_split_kernel(con
       ++seq;
       continue;
     }
-    const int seg = static_cast<int>((cur - base) / nu);
-    const int u0 = static_cast<int>((cur - base) - static_cast<long long>(seg) * nu);
+    const int in_line = static_cast<int>((cur - base) / nu);
+    const int u0 = static_cast<int>((cur - base) - static_cast<long long>(in_line) * nu);
+    const int seg = in_line * a.abreast + beside;
     const int u1 = static_cast<int>(min(static_cast<long long>(nu), u0 + (hi - cur)));
     const int kvh = seg / a.row_groups, h0 = (seg - kvh * a.row_groups) * kRow * kNt;   // first head of the group
     const int32_t* table = a.page_table + seq * a.table_ld;
@@ -417,9 +423,14 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) paged_split_kernel(con
 // Joins the pieces of one segment's row: grid (batch * segments, rows of a segment).
 template <int kDim, int kNt>
 __global__ void __launch_bounds__(kThreads) paged_join_kernel(const PagedArgs a) {
+  constexpr int kShares = kThreads / kDim;   // threads per element: each takes every kShares-th piece
   __shared__ long long sh[2][kWarps];
-  const int segs = a.cache.heads * a.row_groups;
-  const int seq = blockIdx.x / segs, seg = blockIdx.x - seq * segs;
+  __shared__ float sh_red[kWarps];
+  __shared__ float sh_weight[kMaxRanges];
+  __shared__ float sh_sum[kShares][kDim];
+  const int tid = threadIdx.x;
+  const int per_seq = a.cache.heads * a.row_groups, segs = per_seq / a.abreast;
+  const int seq = blockIdx.x / per_seq, seg = blockIdx.x - seq * per_seq;
   const int kvh = seg / a.row_groups, h = (seg - kvh * a.row_groups) * kRow * kNt + blockIdx.y;
   long long mine = 0, all = 0;
   for (int s = threadIdx.x; s < a.batch; s += kThreads) {
@@ -429,33 +440,63 @@ __global__ void __launch_bounds__(kThreads) paged_join_kernel(const PagedArgs a)
   }
   const long long total = block_sum(all, sh[0]) * segs;
   const long long nu = units_of(clamped_len(a, seq));
-  const long long first = block_sum(mine, sh[1]) * segs + seg * nu;
+  const long long first = block_sum(mine, sh[1]) * segs + seg / a.abreast * nu;
   pdl_wait();
-  const int d = threadIdx.x;
-  if (h >= a.group || d >= a.cache.head_dim) return;
+  if (h >= a.group) return;
+  const int d = tid % kDim, share = tid / kDim;
   __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.out.data) + seq * a.out.token_ld +
                        (static_cast<long long>(kvh) * a.group + h) * a.out.head_ld + d;
+  const bool writes = share == 0 && d < a.cache.head_dim;
   if (nu == 0) {
-    *dst = __float2bfloat16(0.0f);
+    if (writes) *dst = __float2bfloat16(0.0f);
     return;
   }
-  // block b holds units [total b / blocks, total (b + 1) / blocks)
+  // range b holds units [total b / blocks, total (b + 1) / blocks)
   const int blocks = blocks_for(total, a.grid);
   const long long b0 = ((first + 1) * blocks - 1) / total, b1 = ((first + nu) * blocks - 1) / total;
   if (b0 == b1) return;   // written by that block
-  float top = -INFINITY, sum = 0.0f, tot = 0.0f;
-  for (long long b = b0; b <= b1; ++b) {
-    // the first block's piece is its last one, unless its range begins there
-    const int slot = b == b0 && total * b / blocks != first ? 1 : 0;
-    const float* part = a.scratch + (b * 2 + slot) * partial_floats<kDim, kNt>();
-    const float pm = part[kRow * kNt * kDim + blockIdx.y], pl = part[kRow * kNt * (kDim + 1) + blockIdx.y];
-    const float po = part[blockIdx.y * kDim + d];
-    const float up = fmaxf(top, pm);
-    const float f = exp2_from(top, up), g = exp2_from(pm, up);
-    sum = sum * f + po * g;
-    tot = tot * f + pl * g;
-    top = up;
+  const int pieces = static_cast<int>(b1 - b0) + 1;
+  // the first block's piece is its last one, unless its range begins there
+  const int slot0 = total * b0 / blocks != first ? 1 : 0;
+  auto piece = [&](int i) {
+    return a.scratch +
+           (((b0 + i) * a.abreast + seg % a.abreast) * 2 + (i == 0 ? slot0 : 0)) * partial_floats<kDim, kNt>();
+  };
+  // all maxima and totals at once, then the weighted sums in independent loads
+  float top = -INFINITY;
+  for (int i = tid; i < pieces; i += kThreads) {
+    sh_weight[i] = piece(i)[kRow * kNt * kDim + blockIdx.y];
+    top = fmaxf(top, sh_weight[i]);
   }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  if ((tid & 31) == 0) sh_red[tid >> 5] = top;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) top = fmaxf(top, sh_red[w]);
+  __syncthreads();
+  float tot = 0.0f;
+  for (int i = tid; i < pieces; i += kThreads) {
+    const float f = exp2_from(sh_weight[i], top);
+    sh_weight[i] = f;
+    tot = fmaf(f, piece(i)[kRow * kNt * (kDim + 1) + blockIdx.y], tot);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) tot += __shfl_xor_sync(0xffffffffu, tot, o);
+  if ((tid & 31) == 0) sh_red[tid >> 5] = tot;
+  __syncthreads();
+  tot = 0.0f;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) tot += sh_red[w];
+  float sum = 0.0f;
+#pragma unroll 8
+  for (int i = share; i < pieces; i += kShares) sum = fmaf(sh_weight[i], d < a.cache.head_dim ? piece(i)[blockIdx.y * kDim + d] : 0.0f, sum);
+  sh_sum[share][d] = sum;
+  __syncthreads();
+  if (!writes) return;
+  sum = 0.0f;
+#pragma unroll
+  for (int i = 0; i < kShares; ++i) sum += sh_sum[i][d];
   *dst = __float2bfloat16(tot == 0.0f ? 0.0f : sum / tot);
 }
 
@@ -463,10 +504,13 @@ template <int kDim, int kNt, int kStages>
 cudaError_t launch_one(PagedArgs a, cudaStream_t st) {
   constexpr int smem = PagedShared<kDim, kNt, kStages>::kBytes;
   a.row_groups = (a.group + kRow * kNt - 1) / (kRow * kNt);
+  const int per_seq = a.cache.heads * a.row_groups;
+  a.abreast = per_seq % 8 == 0 ? 8 : (per_seq % 4 == 0 ? 4 : (per_seq % 2 == 0 ? 2 : 1));
+  a.grid = std::min(kBlocksPerSm * num_sms() / a.abreast, kMaxRanges);
   cudaError_t e = cudaFuncSetAttribute(paged_split_kernel<kDim, kNt, kStages>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  paged_split_kernel<kDim, kNt, kStages><<<a.grid, kThreads, smem, st>>>(a);
+  paged_split_kernel<kDim, kNt, kStages><<<a.grid * a.abreast, kThreads, smem, st>>>(a);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
@@ -501,7 +545,6 @@ cudaError_t launch_paged(const svdq_heads& q, const svdq_kv_cache& cache, const 
   a.scale_log2 = scale * 1.4426950408889634f;
   a.scratch = static_cast<float*>(scratch);
   a.status = device_status_word();
-  a.grid = kBlocksPerSm * num_sms();
   // Up to 8 query heads per key head fill one column tile; more take two, which
   // halves the reads of the cache.
   if (cache.head_dim <= 64) return a.group <= kRow ? launch_one<64, 1, 6>(a, stream) : launch_one<64, 2, 6>(a, stream);
