@@ -512,7 +512,8 @@ svdq_status svdq_attention_prompt(svdq_heads q, svdq_heads k, svdq_heads v, cons
  *              table_ld * page_size records SVDQ_EINVAL and is read as 0 or that limit.
  *   workspace  svdq_attention_decode_workspace_size bytes (16-byte aligned)
  * The split of the work depends on the lengths alone, so results repeat bit for bit.
- * Host errors: SVDQ_EINVAL, SVDQ_EUNSUPPORTED (head_dim, alignment), SVDQ_EWORKSPACE.
+ * Host errors: SVDQ_EINVAL, SVDQ_EUNSUPPORTED (head_dim, alignment, batch * kv_heads *
+ * table_ld * page_size / 16 over 2^31), SVDQ_EWORKSPACE.
  */
 svdq_status svdq_attention_decode(svdq_heads q, const svdq_kv_cache* cache, const int32_t* page_table,
                                   int64_t table_ld, const int32_t* kv_len, int32_t batch, float scale,

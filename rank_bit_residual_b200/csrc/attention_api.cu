@@ -170,7 +170,7 @@ svdq_status svdq_attention_decode_workspace_size(int32_t batch, int32_t heads, i
   if (!bytes) return SVDQ_EINVAL;
   const svdq_status s = check_decode_sizes(batch, heads, kv_heads, head_dim);
   if (s != SVDQ_OK) return s;
-  *bytes = paged_scratch_bytes(heads, kv_heads, head_dim);
+  *bytes = paged_scratch_bytes(batch, heads, kv_heads, head_dim);
   return SVDQ_OK;
 }
 
@@ -186,9 +186,12 @@ svdq_status svdq_attention_decode(svdq_heads q, const svdq_kv_cache* cache, cons
   if (!kv_len || (!page_table && table_ld > 0) || absent(q)) return SVDQ_EINVAL;
   if ((s = check_pair(q, out, cache->head_dim, 2)) != SVDQ_OK) return s;
   if (out.data == q.data) return SVDQ_EINVAL;
-  if (!workspace || workspace_bytes < paged_scratch_bytes(q.heads, cache->heads, cache->head_dim))
+  if (!workspace || workspace_bytes < paged_scratch_bytes(batch, q.heads, cache->heads, cache->head_dim))
     return SVDQ_EWORKSPACE;
   if (!aligned16(workspace)) return SVDQ_EUNSUPPORTED;
+  const int64_t limit = (int64_t(1) << 31) - 1;   // of a sequence's keys, whatever the table could hold
+  const int64_t most = table_ld > limit / cache->page_size ? limit : table_ld * cache->page_size;
+  if (!paged_fits(batch, q.heads, cache->heads, most)) return SVDQ_EUNSUPPORTED;
   return from_cuda(launch_paged(q, *cache, page_table, table_ld, kv_len, batch, scale, out, workspace,
                                 reinterpret_cast<cudaStream_t>(stream)));
 }

@@ -159,7 +159,9 @@ cudaError_t launch_prompt(const svdq_heads& q, const svdq_heads& k, const svdq_h
                           bool causal, float scale, const svdq_heads& out, cudaStream_t stream, bool* bad_args);
 
 // Attention of one token per sequence over a paged cache (paged_attention.cu).
-size_t paged_scratch_bytes(int heads, int kv_heads, int head_dim);
+size_t paged_scratch_bytes(int batch, int heads, int kv_heads, int head_dim);
+// Whether the kernel's 32-bit counts hold for sequences of at most most_keys keys.
+bool paged_fits(int batch, int heads, int kv_heads, int64_t most_keys);
 cudaError_t launch_paged(const svdq_heads& q, const svdq_kv_cache& cache, const int32_t* page_table,
                          int64_t table_ld, const int32_t* kv_len, int batch, float scale, const svdq_heads& out,
                          void* scratch, cudaStream_t stream);

@@ -20,9 +20,13 @@
 // of the first product to the operand layout of the second by a transposing register move.
 //
 // A segment that one block finishes is written at once. Pieces of a segment cut by a
-// block boundary go to the workspace (sums in fp32, maximum, total) and a second kernel,
-// launched as a dependent of the first, joins them in the order of the blocks: the
-// result depends on the lengths alone.
+// block boundary go to the workspace (sums in fp32, maximum, total), with a note of the first
+// and the last range of the segment, and a second kernel, launched as a dependent of the
+// first, joins them in the order of the ranges: the result depends on the lengths alone.
+//
+// One sequence alone costs latency: lengths, pages, keys and the join wait for one another.
+// So both kernels keep to 32-bit arithmetic and few barriers (64-bit divisions and a loop
+// over pieces whose loads waited for one another took 14 of 24 us).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -52,7 +56,10 @@ struct PagedArgs {
   int group;        // query heads per key head
   int row_groups;   // segments per (sequence, key head): ceil(group / (8 * kNt))
   float scale_log2; // scale * log2(e)
-  float* scratch;
+  float* scratch;   // partial results: [range][segment beside][2]
+  int2* ends;       // [sequence][segment]: twice the first range with a piece of it, plus that
+                    // piece's slot, and twice the last
+  int page_shift;   // log2(page_size), or -1
   unsigned* status;
   int abreast;      // segments of a sequence that share the line: 8, 4, 2 or 1
   int grid;         // ranges of the line at most: blocks of the first kernel / abreast
@@ -99,22 +106,29 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-// Ranges that share `total` units: none has less than a unit for each warp unless
-// there is no more than that altogether. 0 without any unit.
-__device__ __forceinline__ int blocks_for(long long total, int grid) {
-  return static_cast<int>(min(static_cast<long long>(grid), (total + kWarps - 1) / kWarps));
+// Ranges that share `total` units: none has less than a unit for each warp unless there is
+// no more than that altogether. 0 without any unit.
+__device__ __forceinline__ int ranges_for(unsigned total, int grid) {
+  return static_cast<int>(min(static_cast<unsigned>(grid), (total + kWarps - 1) / kWarps));
 }
 
-// Sum of v over the block, to all threads. Two calls need a barrier between them.
-__device__ __forceinline__ long long block_sum(long long v, long long* sh) {
+// Inclusive scan over the block. Two calls need a barrier between them.
+__device__ __forceinline__ unsigned block_scan(unsigned v, unsigned* sh, unsigned* sum) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = v;
+  for (int o = 1; o < 32; o <<= 1) {
+    const unsigned up = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += up;
+  }
+  if (lane == 31) sh[warp] = v;
   __syncthreads();
-  long long t = 0;
+  *sum = 0;
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) t += sh[w];
-  return t;
+  for (int w = 0; w < kWarps; ++w) {
+    if (w < warp) v += sh[w];
+    *sum += sh[w];
+  }
+  return v;
 }
 
 template <int kDim, int kNt, int kStages>
@@ -129,57 +143,57 @@ template <int kDim, int kNt, int kStages>
 __global__ void __launch_bounds__(kThreads, kBlocksPerSm) paged_split_kernel(const PagedArgs a) {
   using Sh = PagedShared<kDim, kNt, kStages>;
   extern __shared__ __align__(128) unsigned char smem[];
-  __shared__ long long sh_sum[kWarps];
-  __shared__ long long sh_base;
+  __shared__ unsigned sh_scan[2][kWarps];
+  __shared__ unsigned sh_base;
   __shared__ int sh_seq;
   __shared__ float sh_m[kWarps][kRow * kNt], sh_l[kWarps][kRow * kNt];
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   pdl_trigger();
 
-  // this block's range [lo, hi) of the line of units, and the sequence it begins in
-  const int segs = a.cache.heads * a.row_groups / a.abreast;   // of the line, per sequence
+  // this block's range [lo, hi) of the line of units, and the sequence it begins in; all
+  // units together are below 2^31
+  const unsigned segs = a.cache.heads * a.row_groups / a.abreast;   // of the line, per sequence
   const int range = blockIdx.x / a.abreast, beside = blockIdx.x - range * a.abreast;
-  long long mine = 0;
-  for (int s = tid; s < a.batch; s += kThreads) {
-    const int len = clamped_len(a, s);
-    if (blockIdx.x == 0 && len != a.kv_len[s]) record_status(a.status, kStatusEinval);
-    mine += units_of(len);
-  }
-  const long long total = block_sum(mine, sh_sum) * segs;
-  const int blocks = blocks_for(total, a.grid);
-  if (range >= blocks) return;
-  const long long lo = total * range / blocks, hi = total * (range + 1) / blocks;
-  long long before = 0;
+  unsigned total = 0, upto = 0, here = 0;   // in sequences' units: all, those before thread's next, its own
   for (int s0 = 0; s0 < a.batch; s0 += kThreads) {
-    __syncthreads();
     const int s = s0 + tid;
-    const long long n = s < a.batch ? units_of(clamped_len(a, s)) : 0;
-    long long incl = n;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long up = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += up;
+    here = 0;
+    if (s < a.batch) {
+      const int len = clamped_len(a, s);
+      if (blockIdx.x == 0 && len != a.kv_len[s]) record_status(a.status, kStatusEinval);
+      here = units_of(len);
     }
-    if (lane == 31) sh_sum[warp] = incl;
-    __syncthreads();
-    long long chunk = 0;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      if (w < warp) incl += sh_sum[w];
-      chunk += sh_sum[w];
+    unsigned sum;
+    if (s0 > 0) __syncthreads();
+    upto = total + block_scan(here, sh_scan[0], &sum);
+    total += sum;
+  }
+  total *= segs;
+  const int ranges = ranges_for(total, a.grid);
+  if (range >= ranges) return;
+  // the first total % ranges of them are one unit longer
+  const unsigned share = total / ranges, longer = total - share * ranges;
+  const unsigned lo = share * range + min(static_cast<unsigned>(range), longer);
+  const unsigned hi = lo + share + (range < longer ? 1 : 0);
+  if (a.batch <= kThreads) {
+    if ((upto - here) * segs <= lo && lo < upto * segs) sh_seq = tid, sh_base = (upto - here) * segs;
+  } else {
+    unsigned before = 0;
+    for (int s0 = 0; s0 < a.batch; s0 += kThreads) {
+      const int s = s0 + tid;
+      here = s < a.batch ? units_of(clamped_len(a, s)) : 0;
+      unsigned sum;
+      __syncthreads();
+      upto = before + block_scan(here, sh_scan[1], &sum);
+      if ((upto - here) * segs <= lo && lo < upto * segs) sh_seq = s, sh_base = (upto - here) * segs;
+      before += sum;
+      if (before * segs > lo) break;   // the same for all threads
     }
-    const long long first = (before + incl - n) * segs, end = (before + incl) * segs;
-    if (first <= lo && lo < end) {
-      sh_seq = s;
-      sh_base = first;
-    }
-    before += chunk;
-    if (before * segs > lo) break;   // the same for all threads
   }
   __syncthreads();
   int seq = sh_seq;
-  long long base = sh_base;
+  unsigned base = sh_base;
 
   unsigned char* ring = smem + warp * kStages * 2 * Sh::kTile;
   const uint32_t ring_u = smem_u32(ring);
@@ -187,35 +201,36 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) paged_split_kernel(con
   const __nv_bfloat16* kc = static_cast<const __nv_bfloat16*>(a.cache.k);
   const __nv_bfloat16* vc = static_cast<const __nv_bfloat16*>(a.cache.v);
 
-  long long cur = lo;
+  unsigned cur = lo;
   while (cur < hi) {
     const int len = clamped_len(a, seq);
-    const int nu = units_of(len);
-    if (cur >= base + static_cast<long long>(nu) * segs) {   // past this sequence (or it is empty)
-      base += static_cast<long long>(nu) * segs;
+    const unsigned nu = units_of(len);
+    if (cur >= base + nu * segs) {   // past this sequence (or it is empty)
+      base += nu * segs;
       ++seq;
       continue;
     }
-    const int in_line = static_cast<int>((cur - base) / nu);
-    const int u0 = static_cast<int>((cur - base) - static_cast<long long>(in_line) * nu);
-    const int seg = in_line * a.abreast + beside;
-    const int u1 = static_cast<int>(min(static_cast<long long>(nu), u0 + (hi - cur)));
+    const unsigned in_line = (cur - base) / nu;
+    const int u0 = static_cast<int>(cur - base - in_line * nu);
+    const int u1 = static_cast<int>(min(nu, u0 + (hi - cur)));
+    const int seg = static_cast<int>(in_line) * a.abreast + beside;
     const int kvh = seg / a.row_groups, h0 = (seg - kvh * a.row_groups) * kRow * kNt;   // first head of the group
     const int32_t* table = a.page_table + seq * a.table_ld;
 
     // unit u of this warp: u0 + warp + 4 i
     const int count = (u1 - u0 - warp + kWarps - 1) / kWarps;
     auto unit_at = [&](int i) { return u0 + warp + kWarps * i; };
+    auto page_of = [&](int key) { return a.page_shift >= 0 ? key >> a.page_shift : key / a.cache.page_size; };
     auto lookup = [&](int i) {   // the page of key (lane % 16) of unit i
       const int key = unit_at(i) * kUnit + (lane & 15);
-      return (i < count && key < len) ? table[key / a.cache.page_size] : -1;
+      return (i < count && key < len) ? table[page_of(key)] : -1;
     };
     auto issue = [&](int i, int page) {
       const int key = unit_at(i) * kUnit + (lane & 15);
       long long off = -1;
       if (key < len) {
         if (page >= 0 && page < a.cache.pages)
-          off = page * a.cache.page_ld + static_cast<long long>(key % a.cache.page_size) * a.cache.slot_ld +
+          off = page * a.cache.page_ld + static_cast<long long>(key - page_of(key) * a.cache.page_size) * a.cache.slot_ld +
                 kvh * a.cache.head_ld;
         else
           record_status(a.status, kStatusEinval);
@@ -388,31 +403,46 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) paged_split_kernel(con
         }
       }
     __syncthreads();
-    const bool whole = u0 == 0 && u1 == nu;
-    float* part = a.scratch + (static_cast<long long>(blockIdx.x) * 2 + (cur == lo ? 0 : 1)) * partial_floats<kDim, kNt>();
+    const bool whole = u0 == 0 && u1 == static_cast<int>(nu);
+    float* part = a.scratch + ((static_cast<long long>(range) * a.abreast + beside) * 2 + (cur == lo ? 0 : 1)) *
+                                  partial_floats<kDim, kNt>();
+    if (tid == 0) {
+      int2* ends = a.ends + static_cast<long long>(seq) * a.cache.heads * a.row_groups + seg;
+      if (u0 == 0) ends->x = 2 * range + (cur == lo ? 0 : 1);
+      if (u1 == static_cast<int>(nu)) ends->y = 2 * range;
+    }
+    if (tid < kRow * kNt) {   // the warps' weights, and with them the total
+      float top = sh_m[0][tid];
+#pragma unroll
+      for (int w = 1; w < kWarps; ++w) top = fmaxf(top, sh_m[w][tid]);
+      float tot = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float f = exp2_from(sh_m[w][tid], top);
+        tot = fmaf(f, sh_l[w][tid], tot);
+        sh_m[w][tid] = f;
+      }
+      sh_l[0][tid] = tot;
+      if (!whole) {
+        part[kRow * kNt * kDim + tid] = top;
+        part[kRow * kNt * (kDim + 1) + tid] = tot;
+      }
+    }
+    __syncthreads();
     for (int idx = tid; idx < kRow * kNt * kDim; idx += kThreads) {
       const int r = idx / kDim, d = idx - r * kDim;
       if (h0 + r >= a.group || d >= dim) continue;
-      float top = sh_m[0][r];
+      float sum = 0.0f;
 #pragma unroll
-      for (int w = 1; w < kWarps; ++w) top = fmaxf(top, sh_m[w][r]);
-      float sum = 0.0f, tot = 0.0f;
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        const float f = exp2_from(sh_m[w][r], top);
-        sum = fmaf(f, reinterpret_cast<const float*>(smem)[w * kRow * kNt * (kDim + 4) + r * (kDim + 4) + d], sum);
-        tot = fmaf(f, sh_l[w][r], tot);
-      }
+      for (int w = 0; w < kWarps; ++w)
+        sum = fmaf(sh_m[w][r], reinterpret_cast<const float*>(smem)[w * kRow * kNt * (kDim + 4) + r * (kDim + 4) + d], sum);
       if (whole) {
+        const float tot = sh_l[0][r];
         static_cast<__nv_bfloat16*>(a.out.data)[seq * a.out.token_ld +
                                                 (static_cast<long long>(kvh) * a.group + h0 + r) * a.out.head_ld + d] =
             __float2bfloat16(tot == 0.0f ? 0.0f : sum / tot);
       } else {
         part[r * kDim + d] = sum;
-        if (d == 0) {
-          part[kRow * kNt * kDim + r] = top;
-          part[kRow * kNt * (kDim + 1) + r] = tot;
-        }
       }
     }
     __syncthreads();   // the ring and the statistics are free again
@@ -424,43 +454,30 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) paged_split_kernel(con
 template <int kDim, int kNt>
 __global__ void __launch_bounds__(kThreads) paged_join_kernel(const PagedArgs a) {
   constexpr int kShares = kThreads / kDim;   // threads per element: each takes every kShares-th piece
-  __shared__ long long sh[2][kWarps];
   __shared__ float sh_red[kWarps];
   __shared__ float sh_weight[kMaxRanges];
   __shared__ float sh_sum[kShares][kDim];
   const int tid = threadIdx.x;
-  const int per_seq = a.cache.heads * a.row_groups, segs = per_seq / a.abreast;
+  const int per_seq = a.cache.heads * a.row_groups;
   const int seq = blockIdx.x / per_seq, seg = blockIdx.x - seq * per_seq;
   const int kvh = seg / a.row_groups, h = (seg - kvh * a.row_groups) * kRow * kNt + blockIdx.y;
-  long long mine = 0, all = 0;
-  for (int s = threadIdx.x; s < a.batch; s += kThreads) {
-    const int n = units_of(clamped_len(a, s));
-    all += n;
-    if (s < seq) mine += n;
-  }
-  const long long total = block_sum(all, sh[0]) * segs;
-  const long long nu = units_of(clamped_len(a, seq));
-  const long long first = block_sum(mine, sh[1]) * segs + seg / a.abreast * nu;
-  pdl_wait();
-  if (h >= a.group) return;
   const int d = tid % kDim, share = tid / kDim;
   __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.out.data) + seq * a.out.token_ld +
                        (static_cast<long long>(kvh) * a.group + h) * a.out.head_ld + d;
-  const bool writes = share == 0 && d < a.cache.head_dim;
-  if (nu == 0) {
-    if (writes) *dst = __float2bfloat16(0.0f);
-    return;
-  }
-  // range b holds units [total b / blocks, total (b + 1) / blocks)
-  const int blocks = blocks_for(total, a.grid);
-  const long long b0 = ((first + 1) * blocks - 1) / total, b1 = ((first + nu) * blocks - 1) / total;
-  if (b0 == b1) return;   // written by that block
-  const int pieces = static_cast<int>(b1 - b0) + 1;
-  // the first block's piece is its last one, unless its range begins there
-  const int slot0 = total * b0 / blocks != first ? 1 : 0;
+  const bool writes = share == 0 && d < a.cache.head_dim && h < a.group;
+  const bool empty = clamped_len(a, seq) == 0;
+  pdl_wait();
+  if (empty && writes) *dst = __float2bfloat16(0.0f);
+  if (empty || h >= a.group) return;
+  const int2 ends = a.ends[blockIdx.x];
+  const int first = ends.x >> 1, slot0 = ends.x & 1, pieces = (ends.y >> 1) - first + 1;
+  if (pieces == 1) return;   // written by the block of that range
+  // all pieces but the first begin their range, and are in slot 0
+  const float* mine =
+      a.scratch + static_cast<long long>(first * a.abreast + seg % a.abreast) * 2 * partial_floats<kDim, kNt>();
+  const int step = 2 * a.abreast * partial_floats<kDim, kNt>();
   auto piece = [&](int i) {
-    return a.scratch +
-           (((b0 + i) * a.abreast + seg % a.abreast) * 2 + (i == 0 ? slot0 : 0)) * partial_floats<kDim, kNt>();
+    return mine + static_cast<long long>(i) * step + (i == 0 ? slot0 * partial_floats<kDim, kNt>() : 0);
   };
   // all maxima and totals at once, then the weighted sums in independent loads
   float top = -INFINITY;
@@ -507,6 +524,7 @@ cudaError_t launch_one(PagedArgs a, cudaStream_t st) {
   const int per_seq = a.cache.heads * a.row_groups;
   a.abreast = per_seq % 8 == 0 ? 8 : (per_seq % 4 == 0 ? 4 : (per_seq % 2 == 0 ? 2 : 1));
   a.grid = std::min(kBlocksPerSm * num_sms() / a.abreast, kMaxRanges);
+  a.ends = reinterpret_cast<int2*>(a.scratch + static_cast<size_t>(a.grid) * a.abreast * 2 * partial_floats<kDim, kNt>());
   cudaError_t e = cudaFuncSetAttribute(paged_split_kernel<kDim, kNt, kStages>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
@@ -528,10 +546,26 @@ cudaError_t launch_one(PagedArgs a, cudaStream_t st) {
 
 }  // namespace
 
-size_t paged_scratch_bytes(int heads, int kv_heads, int head_dim) {
+namespace {
+
+int row_groups_of(int heads, int kv_heads) {
+  const int group = heads / kv_heads, rows = group <= kRow ? kRow : 2 * kRow;
+  return (group + rows - 1) / rows;
+}
+
+}  // namespace
+
+size_t paged_scratch_bytes(int batch, int heads, int kv_heads, int head_dim) {
   const size_t one = heads / kv_heads <= kRow ? (head_dim <= 64 ? partial_floats<64, 1>() : partial_floats<128, 1>())
                                               : (head_dim <= 64 ? partial_floats<64, 2>() : partial_floats<128, 2>());
-  return static_cast<size_t>(kBlocksPerSm) * num_sms() * 2 * one * sizeof(float);
+  return static_cast<size_t>(kBlocksPerSm) * num_sms() * 2 * one * sizeof(float) +
+         static_cast<size_t>(batch) * kv_heads * row_groups_of(heads, kv_heads) * sizeof(int2);
+}
+
+bool paged_fits(int batch, int heads, int kv_heads, int64_t most_keys) {
+  const double units = static_cast<double>(batch) * kv_heads * row_groups_of(heads, kv_heads) *
+                       (static_cast<double>(most_keys) / kUnit + 1);
+  return units < 2147483648.0;
 }
 
 cudaError_t launch_paged(const svdq_heads& q, const svdq_kv_cache& cache, const int32_t* page_table,
@@ -545,6 +579,7 @@ cudaError_t launch_paged(const svdq_heads& q, const svdq_kv_cache& cache, const 
   a.scale_log2 = scale * 1.4426950408889634f;
   a.scratch = static_cast<float*>(scratch);
   a.status = device_status_word();
+  a.page_shift = (cache.page_size & (cache.page_size - 1)) == 0 ? __builtin_ctz(cache.page_size) : -1;
   // Up to 8 query heads per key head fill one column tile; more take two, which
   // halves the reads of the cache.
   if (cache.head_dim <= 64) return a.group <= kRow ? launch_one<64, 1, 6>(a, stream) : launch_one<64, 2, 6>(a, stream);
