@@ -179,10 +179,10 @@ __device__ __forceinline__ uint64_t exp2_poly(uint64_t x) {
              __uint_as_float((__float_as_uint(nh) << 23) + __float_as_uint(ph)));
 }
 
-// The bf16 pairs of a word, infinities and NaN replaced by zero; sets *found then.
-__device__ __forceinline__ uint32_t finite_or_zero(uint32_t w, bool* found) {
-  if ((w & 0x7F80u) == 0x7F80u) w &= 0xFFFF0000u, *found = true;
-  if ((w & 0x7F800000u) == 0x7F800000u) w &= 0xFFFFu, *found = true;
+// The bf16 pair of a word, infinities and NaN replaced by zero.
+__device__ __forceinline__ uint32_t finite_or_zero(uint32_t w) {
+  if ((w & 0x7F80u) == 0x7F80u) w &= 0xFFFF0000u;
+  if ((w & 0x7F800000u) == 0x7F800000u) w &= 0xFFFFu;
   return w;
 }
 
@@ -191,7 +191,7 @@ struct Shape {
   static constexpr int kTile = kKeys * kDim * 2;         // bytes of 128 rows of a head
   static constexpr int kRing = kDim == 128 ? 5 : 10;     // tiles of keys and values in flight
   static constexpr int kSmem = 2 * kTile + kRing * kTile + 1024;
-  static constexpr int kPoly = 1;      // pairs of eight whose exponentials go to the FMA pipe
+  static constexpr int kPoly = 2;      // pairs of eight whose exponentials go to the FMA pipe
   static constexpr int kO = 256;                         // tensor memory columns: S0, S1, O0, O1
 };
 
@@ -462,23 +462,31 @@ __global__ void __launch_bounds__(kThreads, 1)
             ok = mbar_wait_warp(&bar.raw[r.i], (raw_phase >> r.i) & 1, a.status, abort);
             if (!ok) break;
             raw_phase ^= 1u << r.i;
-            bool found = false;
-            const int inside = it.keys - j * kKeys;
-            unsigned char* base = ring + r.i * Sz::kTile;
             // 16-byte pieces in memory order: 8 to a row of 64 elements, whatever the swizzle
-            for (int i = lane; i < Sz::kTile / 16; i += 32) {
-              uint4* w = reinterpret_cast<uint4*>(base + i * 16);
-              if ((i >> 3) % kKeys >= inside) {
-                *w = make_uint4(0, 0, 0, 0);
-              } else {
-                const uint4 x = *w;
-                bool here = false;
-                const uint4 y = make_uint4(finite_or_zero(x.x, &here), finite_or_zero(x.y, &here),
-                                           finite_or_zero(x.z, &here), finite_or_zero(x.w, &here));
-                if (here) *w = y, found = true;
-              }
+            uint4* piece = reinterpret_cast<uint4*>(ring + r.i * Sz::kTile);
+            const int inside = min(kKeys, it.keys - j * kKeys);   // rows of this sequence
+            for (int c = 0; c < kDim / 64; ++c)
+              for (int i = inside * 8 + lane; i < kKeys * 8; i += 32) piece[c * kKeys * 8 + i] = make_uint4(0, 0, 0, 0);
+            __syncwarp();
+            // an exponent of all ones carries into the sign bit
+            constexpr int kBatch = 8;
+            uint32_t carried = 0;
+            for (int i = lane; i < Sz::kTile / 16; i += 32 * kBatch) {
+              uint4 x[kBatch];
+#pragma unroll
+              for (int b = 0; b < kBatch; ++b) x[b] = piece[i + 32 * b];
+#pragma unroll
+              for (int b = 0; b < kBatch; ++b)
+                carried |= ((x[b].x & 0x7F807F80u) + 0x00800080u) | ((x[b].y & 0x7F807F80u) + 0x00800080u) |
+                           ((x[b].z & 0x7F807F80u) + 0x00800080u) | ((x[b].w & 0x7F807F80u) + 0x00800080u);
             }
-            if (found) odd[number % (2 * kItems)] = number;
+            if (__any_sync(0xffffffffu, (carried & 0x80008000u) != 0)) {   // hardly ever
+              for (int i = lane; i < Sz::kTile / 16; i += 32) {
+                const uint4 x = piece[i];
+                piece[i] = make_uint4(finite_or_zero(x.x), finite_or_zero(x.y), finite_or_zero(x.z), finite_or_zero(x.w));
+              }
+              odd[number % (2 * kItems)] = number;
+            }
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar.full[r.i]);
@@ -515,15 +523,21 @@ __global__ void __launch_bounds__(kThreads, 1)
       float m = -INFINITY;
       uint64_t sums[2] = {0, 0};   // two pairs of partial sums
       bool ok = true;
+      // S of the next part was complete in time: its first half is being loaded already. (A
+      // wait takes some 200 cycles even when there is nothing to wait for.)
+      bool ahead = false;
+      uint32_t s[2][32];
       for (int j = 0; j < n; ++j) {
         const int buf = j & 1;
         const uint32_t ts = tmem + lanes + t * kKeys + buf * kPart;
-        ok = mbar_wait_soon_warp(&bar.s_full[t][buf], (s_phase >> buf) & 1, a.status, abort);
-        if (!ok) break;
+        if (!ahead) {
+          ok = mbar_wait_soon_warp(&bar.s_full[t][buf], (s_phase >> buf) & 1, a.status, abort);
+          if (!ok) break;
+          tc_fence_after();
+          tmem_ld_32x32b_x32(ts, s[0]);
+        }
         s_phase ^= 1u << buf;
-        tc_fence_after();
-        uint32_t s[2][32];
-        tmem_ld_32x32b_x32(ts, s[0]);
+        ahead = false;
         tmem_ld_wait_regs(s[0]);
         tmem_ld_32x32b_x32(ts + 32, s[1]);
         // weights of half a part with the maximum m; kPoly pairs of eight by polynomial
@@ -563,12 +577,20 @@ __global__ void __launch_bounds__(kThreads, 1)
           largest(0, tops);
           weights(0, std::integral_constant<int, Sz::kPoly>{}, scale2, base2, add);
           tmem_ld_wait_regs(s[1]);
+          const bool there = j + 1 < n && mbar_test(&bar.s_full[t][buf ^ 1], (s_phase >> (buf ^ 1)) & 1);
           largest(1, tops);
           weights(1, std::integral_constant<int, Sz::kPoly>{}, scale2, base2, add);
           // (a row that has seen nothing but -inf, m = -inf, is not done either)
           const float top = max3_nan(tops[0], tops[1], tops[1]) * scale;
           done = __all_sync(0xffffffffu, top <= m + 8.0f && m > -INFINITY);
-          if (done) sums[0] = add[0], sums[1] = add[1];
+          if (done) {
+            sums[0] = add[0], sums[1] = add[1];
+            ahead = __all_sync(0xffffffffu, there);
+            if (ahead) {
+              tc_fence_after();
+              tmem_ld_32x32b_x32(ts ^ kPart, s[0]);
+            }
+          }
         } else {
           tmem_ld_wait_regs(s[1]);
         }
