@@ -490,13 +490,19 @@ svdq_status svdq_kv_append(const svdq_kv_cache* cache, svdq_heads k, svdq_heads 
  *   scale      finite, e.g. 1 / sqrt(head_dim)
  *   out        [q_tokens, heads, head_dim], must not overlap an input. A row that sees
  *              no key becomes zero. Rows of no sequence are left as they were.
- * Host errors: SVDQ_EINVAL, SVDQ_EUNSUPPORTED (head_dim, alignment; q_tokens,
- * k_tokens, batch over 2^24, heads * (q_tokens / 64 + batch) over 2^30).
+ *   workspace  svdq_attention_prompt_workspace_size bytes (16-byte aligned; 0 bytes, and
+ *              NULL, unless few rows meet many keys)
+ * How the work is divided depends on the sizes alone, so results repeat bit for bit.
+ * Host errors: SVDQ_EINVAL, SVDQ_EUNSUPPORTED (head_dim, alignment; q_tokens, k_tokens
+ * or batch over 2^24, heads * (q_tokens / 64 + batch) over 2^30), SVDQ_EWORKSPACE.
  */
 svdq_status svdq_attention_prompt(svdq_heads q, svdq_heads k, svdq_heads v, const int32_t* cu_q,
                                   const int32_t* cu_k, int32_t batch, int64_t q_tokens, int64_t k_tokens,
                                   int32_t head_dim, int32_t causal, float scale, svdq_heads out,
-                                  svdq_stream_t stream);
+                                  void* workspace, size_t workspace_bytes, svdq_stream_t stream);
+
+svdq_status svdq_attention_prompt_workspace_size(int32_t heads, int32_t kv_heads, int32_t head_dim, int32_t batch,
+                                                 int64_t q_tokens, int64_t k_tokens, size_t* bytes);
 
 /*
  * svdq_attention_decode - attention of one new token per sequence over a paged cache

@@ -100,7 +100,8 @@ _SIGS = {
     "svdq_kv_append": (c_i32, [ctypes.POINTER(SvdqKvCache), SvdqHeads, SvdqHeads, c_vp, c_i64, c_vp, SvdqRope, c_vp,
                                c_i32, ctypes.c_float, SvdqHeads, c_vp, SvdqHeads, SvdqHeads, c_vp]),
     "svdq_attention_prompt": (c_i32, [SvdqHeads, SvdqHeads, SvdqHeads, c_vp, c_vp, c_i32, c_i64, c_i64, c_i32, c_i32,
-                                      ctypes.c_float, SvdqHeads, c_vp]),
+                                      ctypes.c_float, SvdqHeads, c_vp, c_sz, c_vp]),
+    "svdq_attention_prompt_workspace_size": (c_i32, [c_i32, c_i32, c_i32, c_i32, c_i64, c_i64, ctypes.POINTER(c_sz)]),
     "svdq_attention_decode": (c_i32, [SvdqHeads, ctypes.POINTER(SvdqKvCache), c_vp, c_i64, c_vp, c_i32,
                                       ctypes.c_float, SvdqHeads, c_vp, c_sz, c_vp]),
     "svdq_attention_decode_workspace_size": (c_i32, [c_i32, c_i32, c_i32, c_i32, ctypes.POINTER(c_sz)]),

@@ -317,17 +317,28 @@ def svdq_kv_append(k_cache: torch.Tensor, v_cache: torch.Tensor, k: torch.Tensor
     return q_out
 
 
+@functools.lru_cache(maxsize=4096)
+def _prompt_scratch(dev: int, heads: int, kv_heads: int, dim: int, batch: int, q_tokens: int, k_tokens: int) -> int:
+    size = c_sz()
+    _check(load_library().svdq_attention_prompt_workspace_size(heads, kv_heads, dim, batch, q_tokens, k_tokens,
+                                                               ctypes.byref(size)),
+           "svdq_attention_prompt_workspace_size")
+    return size.value
+
+
 @_on_device
 def svdq_attention_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: Optional[torch.Tensor] = None,
                           cu_k: Optional[torch.Tensor] = None, causal: bool = True,
-                          scale: Optional[float] = None, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+                          scale: Optional[float] = None, out: Optional[torch.Tensor] = None,
+                          workspace: Optional[LinearWorkspace] = None) -> torch.Tensor:
     """Attention over packed sequences: q [Tq, H, D], k and v [Tk, Hkv, D], bf16.
 
     cu_q, cu_k int32 [batch + 1]: sequence s owns rows cu[s] .. cu[s + 1] - 1 (None: one
     sequence of all rows). causal: rows and keys of a sequence end together, and a row
     sees no key behind its own place; a row that sees none becomes zero. Rows of no
     sequence are left as they were in `out`, and mean nothing in an output allocated here.
-    Returns [Tq, H, D].
+    Scratch (few rows over many keys need some) is allocated per call unless a workspace
+    is given (one per stream in flight). Returns [Tq, H, D].
     """
     dev = _device(q, k, v, cu_q, cu_k, out)
     qs, ks, vs = _shape3(q, "q", _BF16), _shape3(k, "k", _BF16), _shape3(v, "v", _BF16)
@@ -355,9 +366,12 @@ def svdq_attention_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_
     vd, v = _heads(v, vs)
     cu_q = None if cu_q is None else cu_q.contiguous()
     cu_k = None if cu_k is None else cu_k.contiguous()
+    size, ws = _prompt_scratch(dev, H, ks[1], D, batch, T, ks[0]), None
+    if size:
+        ws = q.new_empty(size, dtype=torch.uint8) if workspace is None else workspace.get(size, q.device)
     st = load_library().svdq_attention_prompt(
         qd, kd, vd, None if cu_q is None else cu_q.data_ptr(), None if cu_k is None else cu_k.data_ptr(), batch, T,
-        ks[0], D, 1 if causal else 0, scale, qo, _raw_stream(dev))
+        ks[0], D, 1 if causal else 0, scale, qo, None if ws is None else ws.data_ptr(), size, _raw_stream(dev))
     if st:
         _check(st, "svdq_attention_prompt")
     return out
@@ -463,5 +477,6 @@ class AttentionStep:
         else:
             # rows of no sequence must not reach the next projection: its scale is the maximum over all rows
             o = torch.zeros((T, H, D), dtype=qkv.dtype, device=qkv.device) if self.cu_seqlens is not None else None
-            o = svdq_attention_prompt(q, k, v, self.cu_seqlens, self.cu_seqlens, self.causal, self.scale, out=o)
+            o = svdq_attention_prompt(q, k, v, self.cu_seqlens, self.cu_seqlens, self.causal, self.scale, out=o,
+                                      workspace=self.workspace)
         return o.view(T, H * D)

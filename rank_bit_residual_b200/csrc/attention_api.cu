@@ -78,6 +78,18 @@ svdq_status check_decode_sizes(int32_t batch, int32_t heads, int32_t kv_heads, i
   return check_dim(head_dim, 128);
 }
 
+svdq_status check_prompt_sizes(int32_t heads, int32_t kv_heads, int32_t head_dim, int32_t batch, int64_t q_tokens,
+                               int64_t k_tokens) {
+  if (batch < 0 || q_tokens < 0 || k_tokens < 0 || heads < 1 || kv_heads < 1 || heads % kv_heads != 0)
+    return SVDQ_EINVAL;
+  const svdq_status s = check_dim(head_dim, 128);
+  if (s != SVDQ_OK) return s;
+  if (heads > kMaxHeads || q_tokens > kMaxPrompt || k_tokens > kMaxPrompt || batch > kMaxPrompt ||
+      heads * (q_tokens / 64 + batch) > (int64_t(1) << 30))
+    return SVDQ_EUNSUPPORTED;
+  return SVDQ_OK;
+}
+
 }  // namespace
 
 }  // namespace svdq
@@ -137,30 +149,37 @@ svdq_status svdq_kv_append(const svdq_kv_cache* cache, svdq_heads k, svdq_heads 
   return from_cuda(launch_heads(a, SVDQ_BF16, reinterpret_cast<cudaStream_t>(stream)));
 }
 
+svdq_status svdq_attention_prompt_workspace_size(int32_t heads, int32_t kv_heads, int32_t head_dim, int32_t batch,
+                                                 int64_t q_tokens, int64_t k_tokens, size_t* bytes) {
+  if (!bytes) return SVDQ_EINVAL;
+  const svdq_status s = check_prompt_sizes(heads, kv_heads, head_dim, batch, q_tokens, k_tokens);
+  if (s != SVDQ_OK) return s;
+  *bytes = batch == 0 || q_tokens == 0 ? 0 : prompt_scratch_bytes(heads, kv_heads, head_dim, batch, q_tokens, k_tokens);
+  return SVDQ_OK;
+}
+
 svdq_status svdq_attention_prompt(svdq_heads q, svdq_heads k, svdq_heads v, const int32_t* cu_q,
                                   const int32_t* cu_k, int32_t batch, int64_t q_tokens, int64_t k_tokens,
                                   int32_t head_dim, int32_t causal, float scale, svdq_heads out,
-                                  svdq_stream_t stream) {
-  if (batch < 0 || q_tokens < 0 || k_tokens < 0 || (causal != 0 && causal != 1) || !std::isfinite(scale))
-    return SVDQ_EINVAL;
-  svdq_status s = check_dim(head_dim, 128);
+                                  void* workspace, size_t workspace_bytes, svdq_stream_t stream) {
+  if ((causal != 0 && causal != 1) || !std::isfinite(scale)) return SVDQ_EINVAL;
+  svdq_status s = check_prompt_sizes(q.heads, k.heads, head_dim, batch, q_tokens, k_tokens);
   if (s != SVDQ_OK) return s;
   if (batch == 0 || q_tokens == 0) return SVDQ_OK;
   if ((!cu_q || !cu_k) && batch != 1) return SVDQ_EINVAL;
   if ((s = check_pair(q, out, head_dim, 2)) != SVDQ_OK) return s;
-  if (absent(q) || out.data == q.data) return SVDQ_EINVAL;
+  if (absent(q) || out.data == q.data || k.heads != v.heads) return SVDQ_EINVAL;
   // no keys at all: the tensors need not exist, the rows become zero
   if (k_tokens > 0) {
     if ((s = check_heads(k, head_dim, 2)) != SVDQ_OK) return s;
     if ((s = check_heads(v, head_dim, 2)) != SVDQ_OK) return s;
   }
-  if (k.heads < 1 || k.heads != v.heads || q.heads % k.heads != 0) return SVDQ_EINVAL;
-  if (q_tokens > kMaxPrompt || k_tokens > kMaxPrompt || batch > kMaxPrompt ||
-      q.heads * (q_tokens / 64 + batch) > (int64_t(1) << 30))
-    return SVDQ_EUNSUPPORTED;
+  const size_t need = prompt_scratch_bytes(q.heads, k.heads, head_dim, batch, q_tokens, k_tokens);
+  if (need > 0 && (!workspace || workspace_bytes < need)) return SVDQ_EWORKSPACE;
+  if (need > 0 && !aligned16(workspace)) return SVDQ_EUNSUPPORTED;
   bool bad = false;
   const cudaError_t e = launch_prompt(q, k, v, cu_q, cu_k, batch, q_tokens, k_tokens, head_dim, causal != 0, scale,
-                                      out, reinterpret_cast<cudaStream_t>(stream), &bad);
+                                      out, workspace, reinterpret_cast<cudaStream_t>(stream), &bad);
   if (bad) return SVDQ_EUNSUPPORTED;
   return from_cuda(e);
 }

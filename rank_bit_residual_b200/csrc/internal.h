@@ -153,10 +153,13 @@ struct HeadsArgs {
 };
 cudaError_t launch_heads(const HeadsArgs& a, svdq_dtype dtype, cudaStream_t stream);
 
-// Attention over packed prompts (prompt_attention.cu).
+// Attention over packed prompts (prompt_attention.cu). scratch holds prompt_scratch_bytes(...)
+// bytes (0 where the keys are not divided).
+size_t prompt_scratch_bytes(int heads, int kv_heads, int head_dim, int batch, int64_t q_tokens, int64_t k_tokens);
 cudaError_t launch_prompt(const svdq_heads& q, const svdq_heads& k, const svdq_heads& v, const int32_t* cu_q,
                           const int32_t* cu_k, int batch, int64_t q_tokens, int64_t k_tokens, int head_dim,
-                          bool causal, float scale, const svdq_heads& out, cudaStream_t stream, bool* bad_args);
+                          bool causal, float scale, const svdq_heads& out, void* scratch, cudaStream_t stream,
+                          bool* bad_args);
 
 // Attention of one token per sequence over a paged cache (paged_attention.cu).
 size_t paged_scratch_bytes(int batch, int heads, int kv_heads, int head_dim);

@@ -25,6 +25,10 @@
 // items balance), 10 cleans values: in tiles that hold a key some row does not see,
 // rows behind the sequence's end become zero, and infinities and NaN too (a zero weight
 // must not meet them); the latter are added at the end to the rows that do see them.
+//
+// Few rows over many keys would leave most SMs idle: the keys of an item are then divided
+// among several items, whose unfinished sums a second kernel joins (301 rows over 7501 keys,
+// 48 items: 108 -> 68 us with three shares).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -43,6 +47,7 @@ constexpr int kRows = 128;      // query rows of a tile
 constexpr int kKeys = 128;      // keys of a loaded tile
 constexpr int kPart = 64;       // keys of a part: what softmax takes at a time
 constexpr int kThreads = 384;
+constexpr int kMaxShares = 8;   // items that divide an item's keys
 constexpr int kItems = 4;       // items between the chooser and the slowest reader
 
 struct PromptArgs {
@@ -54,6 +59,8 @@ struct PromptArgs {
   int dim, causal;
   int tile_rows;    // rows of a sequence that an item covers: 128 (two heads) or 256
   int pairs;        // items per row range: heads / 2 or heads
+  int shares;       // items that divide an item's keys
+  float* partial;   // with several shares: [item][share][tile] sums [dim][128], maxima [128], totals [128]
   float scale_log2;
   unsigned* status;
 };
@@ -68,6 +75,7 @@ struct Item {
   int rows[2];      // rows inside the sequence, 0 .. 128
   int head[2];
   int seen[2];      // keys that the tile's first row sees (causal; row r sees r more)
+  int index;        // of the item and its share
 };
 
 // Start of sequence s (no list: one sequence of all rows).
@@ -84,9 +92,11 @@ __device__ __forceinline__ bool bad_cu(const int32_t* cu, int s, long long token
 // whole warp calls it; valid = 0 past the last range.
 __device__ Item find_item(const PromptArgs& a, int index) {
   const int lane = threadIdx.x & 31;
-  const int range = index / a.pairs, pair = index - range * a.pairs;
+  const int whole = index / a.shares, part = index - whole * a.shares;
+  const int range = whole / a.pairs, pair = whole - range * a.pairs;
   Item it;
   it.valid = 0;
+  it.index = index;
   int before = 0;
   for (int s0 = 0; s0 < a.batch; s0 += 32) {
     const int s = s0 + lane;
@@ -118,9 +128,8 @@ __device__ Item find_item(const PromptArgs& a, int index) {
       // the last ranges of a causal sequence see the most keys: they go first
       const int r0 = (n - 1 - (range - first)) * a.tile_rows;
       it.valid = 1;
-      it.keys = keys, it.k0 = k0;
       const bool two_heads = a.tile_rows == kRows;
-      it.cut = 0x7FFFFFFF;
+      int last = 0;   // keys that any row sees
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
         const int row = two_heads ? r0 : r0 + t * kRows;
@@ -128,8 +137,21 @@ __device__ Item find_item(const PromptArgs& a, int index) {
         it.row[t] = q0 + row;
         it.rows[t] = max(0, min(kRows, rows - row));
         it.seen[t] = a.causal ? keys - rows + row + 1 : keys;
-        const int last = a.causal ? min(keys, it.seen[t] + it.rows[t] - 1) : keys;
-        it.n[t] = it.rows[t] > 0 ? max(0, last + kPart - 1) / kPart : 0;
+        if (it.rows[t] > 0) last = max(last, a.causal ? min(keys, it.seen[t] + it.rows[t] - 1) : keys);
+      }
+      if (a.shares > 1) {   // this share's keys become the item's own
+        const int tiles = (last + kKeys - 1) / kKeys;
+        const int from = tiles * part / a.shares * kKeys, to = tiles * (part + 1) / a.shares * kKeys;
+        k0 += from;
+        keys = min(keys, to) - from;
+        it.seen[0] -= from, it.seen[1] -= from;
+      }
+      it.keys = keys, it.k0 = k0;
+      it.cut = 0x7FFFFFFF;
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        const int end = a.causal ? min(keys, it.seen[t] + it.rows[t] - 1) : keys;
+        it.n[t] = it.rows[t] > 0 ? max(0, end + kPart - 1) / kPart : 0;
         it.cut = min(it.cut, max(0, min(keys, it.seen[t])) / kKeys);
       }
       it.kvh = it.head[0] / (a.q.heads / a.k.heads);
@@ -186,12 +208,18 @@ __device__ __forceinline__ uint32_t finite_or_zero(uint32_t w) {
   return w;
 }
 
+// Floats of an unfinished row tile: sums, maxima and totals.
+template <int kDim>
+__host__ __device__ constexpr int partial_floats() {
+  return (kDim + 2) * kRows;
+}
+
 template <int kDim>
 struct Shape {
   static constexpr int kTile = kKeys * kDim * 2;         // bytes of 128 rows of a head
   static constexpr int kRing = kDim == 128 ? 5 : 10;     // tiles of keys and values in flight
   static constexpr int kSmem = 2 * kTile + kRing * kTile + 1024;
-  static constexpr int kPoly = 2;      // pairs of eight whose exponentials go to the FMA pipe
+  static constexpr int kPoly = kDim == 128 ? 2 : 0;      // pairs of eight whose exponentials go to the FMA pipe
   static constexpr int kO = 256;                         // tensor memory columns: S0, S1, O0, O1
 };
 
@@ -215,7 +243,8 @@ struct Turn {
   }
 };
 
-template <int kDim>
+// kShared: the keys of an item are divided, and its sums stay unfinished.
+template <int kDim, bool kShared>
 __global__ void __launch_bounds__(kThreads, 1)
     prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                   const __grid_constant__ CUtensorMap map_v, const __grid_constant__ PromptArgs a) {
@@ -513,6 +542,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const Item& sh = items[slot.i];
       const int valid = sh.valid, keys = sh.keys, k0 = sh.k0, kvh = sh.kvh, n = sh.n[t], cut = sh.cut;
       const int row0 = sh.row[t], rows = sh.rows[t], head = sh.head[t];
+      const int index = kShared ? sh.index : 0;
       const int seen = a.causal ? min(keys, sh.seen[t] + row) : keys;   // keys of this row
       const int all_see = min(keys, sh.seen[t]);
       __syncwarp();
@@ -645,7 +675,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       upk2(sums[0], l4[0], l4[1]);
       upk2(sums[1], l4[2], l4[3]);
       const float l = (l4[0] + l4[1]) + (l4[2] + l4[3]);
-      const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+      float inv = l == 0.0f ? 0.0f : 1.0f / l;
+      float* partial = nullptr;
+      if (kShared) {
+        inv = 1.0f;
+        partial = a.partial + (static_cast<long long>(index) * 2 + t) * partial_floats<kDim>() + row;
+        partial[kDim * kRows] = m;
+        partial[(kDim + 1) * kRows] = l;
+      }
       const bool extra = n > 0 && odd[number % (2 * kItems)] == number;
       __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.out.data) +
                            static_cast<long long>(row0 + row) * a.out.token_ld + head * a.out.head_ld;
@@ -665,6 +702,11 @@ __global__ void __launch_bounds__(kThreads, 1)
               const float x = c * 32 + i < a.dim ? __bfloat162float(vp[(k0 + key) * a.v.token_ld + c * 32 + i]) : 0.0f;
               if (!isfinite(x)) o[i] = __float_as_uint(__uint_as_float(o[i]) + x);
             }
+        }
+        if (kShared) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) partial[(c * 32 + i) * kRows] = n > 0 ? __uint_as_float(o[i]) : 0.0f;
+          continue;
         }
 #pragma unroll
         for (int i = 0; i < 32; i += 8) {
@@ -688,27 +730,106 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
+// Joins the shares of one row tile: grid (items, 2, 4), a thread per row and eighth of the elements.
+constexpr int kJoinThreads = 256;
+template <int kDim>
+__global__ void __launch_bounds__(kJoinThreads) prompt_join_kernel(const __grid_constant__ PromptArgs a) {
+  __shared__ Item sh_item;
+  if (threadIdx.x < 32) {
+    const Item it = find_item(a, blockIdx.x * a.shares);
+    if (threadIdx.x == 0) sh_item = it;
+  }
+  __syncthreads();
+  pdl_wait();
+  const int t = blockIdx.y, row = threadIdx.x % kRows, eighth = blockIdx.z * 2 + threadIdx.x / kRows;
+  if (!sh_item.valid || row >= sh_item.rows[t]) return;
+  const int step = 2 * partial_floats<kDim>();   // from share to share
+  const float* p = a.partial + (static_cast<long long>(blockIdx.x) * a.shares * 2 + t) * partial_floats<kDim>() + row;
+  float top = -INFINITY;
+  for (int s = 0; s < a.shares; ++s) top = fmaxf(top, p[s * step + kDim * kRows]);
+  float weight[kMaxShares], total = 0.0f;
+#pragma unroll
+  for (int s = 0; s < kMaxShares; ++s) {
+    const float m = s < a.shares ? p[s * step + kDim * kRows] : -INFINITY;
+    weight[s] = m == -INFINITY ? 0.0f : exp2f(m - top);
+    if (weight[s] != 0.0f) total = fmaf(weight[s], p[s * step + (kDim + 1) * kRows], total);
+  }
+  const float inv = total == 0.0f ? 0.0f : 1.0f / total;
+  __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.out.data) +
+                       static_cast<long long>(sh_item.row[t] + row) * a.out.token_ld + sh_item.head[t] * a.out.head_ld;
+  for (int d = eighth * (kDim / 8); d < (eighth + 1) * (kDim / 8) && d < a.dim; d += 8) {
+    float x[8] = {};
+#pragma unroll
+    for (int s = 0; s < kMaxShares; ++s)
+      if (weight[s] != 0.0f) {   // a share that saw no key holds nothing
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = fmaf(weight[s], p[s * step + (d + i) * kRows], x[i]);
+      }
+    *reinterpret_cast<uint4*>(dst + d) =
+        make_uint4(pack_bf16(x[0] * inv, x[1] * inv), pack_bf16(x[2] * inv, x[3] * inv),
+                   pack_bf16(x[4] * inv, x[5] * inv), pack_bf16(x[6] * inv, x[7] * inv));
+  }
+}
+
+// How an item is made up, and how many there are at most.
+struct PromptPlan {
+  int tile_rows, pairs, shares;
+  int64_t items;
+};
+
+PromptPlan plan_prompt(int heads, int kv_heads, int batch, int64_t q_tokens, int64_t k_tokens) {
+  PromptPlan p;
+  // Two heads that share their keys make a better pair than two row ranges: both tiles see
+  // the same keys, and a sequence's last range wastes fewer rows.
+  const bool two_heads = heads / kv_heads % 2 == 0;
+  p.tile_rows = two_heads ? kRows : 2 * kRows;
+  p.pairs = two_heads ? heads / 2 : heads;
+  p.items = (q_tokens / p.tile_rows + batch) * p.pairs;
+  // As many shares as fill the SMs once, each of a thousand keys or more on average: below
+  // that the join takes what the shares gain.
+  const int64_t fill = num_sms() / std::max<int64_t>(p.items, 1), keys = k_tokens / std::max(batch, 1) / 1024;
+  p.shares = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({fill, keys, kMaxShares})));
+  return p;
+}
+
 template <int kDim>
 cudaError_t launch_dim(const PromptArgs& a, const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv,
-                       unsigned grid, cudaStream_t st) {
+                       int64_t items, cudaStream_t st) {
   constexpr int smem = Shape<kDim>::kSmem;
-  cudaError_t e = cudaFuncSetAttribute(prompt_kernel<kDim>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  auto* kernel = a.shares > 1 ? prompt_kernel<kDim, true> : prompt_kernel<kDim, false>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  prompt_kernel<kDim><<<grid, kThreads, smem, st>>>(mq, mk, mv, a);
-  return cudaGetLastError();
+  kernel<<<static_cast<unsigned>(items * a.shares), kThreads, smem, st>>>(mq, mk, mv, a);
+  e = cudaGetLastError();
+  if (e != cudaSuccess || a.shares == 1) return e;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(items), 2, 4);
+  cfg.blockDim = dim3(kJoinThreads);
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, prompt_join_kernel<kDim>, a);
 }
 
 }  // namespace
 
+size_t prompt_scratch_bytes(int heads, int kv_heads, int head_dim, int batch, int64_t q_tokens, int64_t k_tokens) {
+  const PromptPlan p = plan_prompt(heads, kv_heads, batch, q_tokens, k_tokens);
+  if (p.shares == 1) return 0;
+  return static_cast<size_t>(p.items) * p.shares * 2 * sizeof(float) *
+         (head_dim <= 64 ? partial_floats<64>() : partial_floats<128>());
+}
+
 cudaError_t launch_prompt(const svdq_heads& q, const svdq_heads& k, const svdq_heads& v, const int32_t* cu_q,
                           const int32_t* cu_k, int batch, int64_t q_tokens, int64_t k_tokens, int head_dim,
-                          bool causal, float scale, const svdq_heads& out, cudaStream_t stream, bool* bad_args) {
-  const int group = q.heads / k.heads;
-  // Two heads that share their keys make a better pair than two row ranges: both tiles see
-  // the same keys, and a sequence's last range wastes fewer rows.
-  const bool two_heads = group % 2 == 0;
+                          bool causal, float scale, const svdq_heads& out, void* scratch, cudaStream_t stream,
+                          bool* bad_args) {
+  const PromptPlan p = plan_prompt(q.heads, k.heads, batch, q_tokens, k_tokens);
   PromptArgs a{q, k, v, out, cu_q, cu_k, batch, q_tokens, k_tokens, head_dim, causal ? 1 : 0,
-               two_heads ? kRows : 2 * kRows, two_heads ? q.heads / 2 : q.heads, scale * 1.4426950408889634f,
+               p.tile_rows, p.pairs, p.shares, static_cast<float*>(scratch), scale * 1.4426950408889634f,
                device_status_word()};
   CUtensorMap mq, mk, mv;
   // without any key no tile of k or v is ever loaded
@@ -716,8 +837,8 @@ cudaError_t launch_prompt(const svdq_heads& q, const svdq_heads& k, const svdq_h
               !make_tmap_heads(&mk, k_tokens > 0 ? k : q, head_dim, k_tokens > 0 ? k_tokens : q_tokens, kKeys) ||
               !make_tmap_heads(&mv, k_tokens > 0 ? v : q, head_dim, k_tokens > 0 ? k_tokens : q_tokens, kKeys);
   if (*bad_args) return cudaSuccess;
-  const unsigned grid = static_cast<unsigned>((q_tokens / a.tile_rows + batch) * a.pairs);
-  return head_dim <= 64 ? launch_dim<64>(a, mq, mk, mv, grid, stream) : launch_dim<128>(a, mq, mk, mv, grid, stream);
+  return head_dim <= 64 ? launch_dim<64>(a, mq, mk, mv, p.items, stream)
+                        : launch_dim<128>(a, mq, mk, mv, p.items, stream);
 }
 
 }  // namespace svdq

@@ -103,10 +103,10 @@ def test_append_unsupported(lib, kw):
 
 
 def prompt(lib, q=None, k=None, v=None, cu_q=P, cu_k=P, batch=2, q_tokens=5, k_tokens=5, dim=64, causal=1, scale=0.1,
-           out=None):
+           out=None, ws=None, ws_bytes=0):
     return lib.svdq_attention_prompt(heads() if q is None else q, heads(2) if k is None else k,
                                      heads(2) if v is None else v, cu_q, cu_k, batch, q_tokens, k_tokens, dim, causal,
-                                     scale, heads(data=2 * P) if out is None else out, None)
+                                     scale, heads(data=2 * P) if out is None else out, ws, ws_bytes, None)
 
 
 @pytest.mark.parametrize("kw", [
@@ -128,6 +128,21 @@ def test_prompt_unsupported(lib, kw):
     if kw.get("dim") == 136:
         kw = dict(kw, q=heads(dim=136), k=heads(2, dim=136), v=heads(2, dim=136), out=heads(dim=136, data=2 * P))
     assert prompt(lib, **kw) == rb.SVDQ_EUNSUPPORTED
+
+
+def test_prompt_workspace(lib):
+    n = ctypes.c_size_t(7)
+    size = lib.svdq_attention_prompt_workspace_size
+    assert size(32, 8, 128, 1, 8192, 8192, ctypes.byref(n)) == rb.SVDQ_OK and n.value == 0
+    assert size(4, 2, 64, 0, 0, 0, ctypes.byref(n)) == rb.SVDQ_OK and n.value == 0
+    assert size(4, 2, 64, 1, 100, 8192, ctypes.byref(n)) == rb.SVDQ_OK and n.value > 0   # few rows, many keys
+    few = dict(batch=1, q_tokens=100, k_tokens=8192)
+    assert prompt(lib, **few) == rb.SVDQ_EWORKSPACE
+    assert prompt(lib, ws=P, ws_bytes=n.value - 1, **few) == rb.SVDQ_EWORKSPACE
+    assert prompt(lib, ws=P + 8, ws_bytes=n.value, **few) == rb.SVDQ_EUNSUPPORTED
+    assert size(4, 3, 64, 1, 100, 8192, ctypes.byref(n)) == rb.SVDQ_EINVAL
+    assert size(4, 2, 60, 1, 100, 8192, ctypes.byref(n)) == rb.SVDQ_EUNSUPPORTED
+    assert size(4, 2, 64, 1, 100, 8192, None) == rb.SVDQ_EINVAL
 
 
 def decode(lib, q=None, c=None, table=P, table_ld=4, kv_len=P, batch=3, scale=0.1, out=None, ws=P, ws_bytes=1 << 30):

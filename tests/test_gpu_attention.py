@@ -1,5 +1,6 @@
 """svdq_attention_prompt and svdq_attention_decode against the float64 definition."""
 
+import ctypes
 import math
 
 import numpy as np
@@ -91,6 +92,36 @@ def test_prompt_growing_scores():
 def test_prompt_long():
     run_prompt([2500, 700], [2500, 700], 2, 1, 128, True, seed=9)
     run_prompt([1500], [4000], 1, 1, 64, False, seed=10)
+
+
+@pytest.mark.parametrize("q_lens,k_lens,H,K", [
+    ([37], [5000], 4, 2), ([1], [9000], 3, 1), ([300], [7501], 6, 2), ([5, 130], [6000, 2500], 4, 4),
+    ([200, 40], [0, 8200], 2, 2), ([2100], [2100], 1, 1),
+])
+@pytest.mark.parametrize("D", [64, 128, 80])
+@pytest.mark.parametrize("causal", [True, False])
+def test_prompt_few_rows_many_keys(q_lens, k_lens, H, K, D, causal):
+    """The keys are divided among blocks and the shares joined."""
+    n = ctypes.c_size_t()
+    lib = rb.load_library()
+    lib.svdq_attention_prompt_workspace_size(H, K, D, len(q_lens), sum(q_lens), sum(k_lens), ctypes.byref(n))
+    assert n.value > 0
+    q, k, v, got = run_prompt(q_lens, k_lens, H, K, D, causal, seed=H + D)
+    cu_q, cu_k = ints(np.cumsum([0] + q_lens)), ints(np.cumsum([0] + k_lens))
+    work = rb.LinearWorkspace()
+    for _ in range(3):                           # the same bits, whatever the scratch holds
+        again = rb.svdq_attention_prompt(q, k, v, cu_q, cu_k, causal=causal, workspace=work)
+        assert torch.equal(again, got)
+        work.buf.fill_(255)
+
+
+def test_prompt_shares_nan_behind_the_mask():
+    q, k, v = draw(1, 100, 2, 64), draw(2, 5000, 1, 64), draw(3, 5000, 1, 64)
+    want = rb.svdq_attention_prompt(q, k, v)
+    k2, v2 = k.clone(), v.clone()
+    k2[4960:], v2[4960:] = float("inf"), float("nan")
+    got = rb.svdq_attention_prompt(q, k2, v2)
+    assert torch.equal(got[:60], want[:60]) and torch.isnan(got[60:]).all()
 
 
 def test_prompt_projection_row_and_outputs():
