@@ -118,15 +118,30 @@ __device__ Item find_item(const PromptArgs& a, int index) {
     }
     const unsigned hit = __ballot_sync(0xffffffffu, before + incl > range);
     if (hit != 0) {
-      const int src = __ffs(hit) - 1;
-      const int first = before + __shfl_sync(0xffffffffu, incl - n, src);
-      n = __shfl_sync(0xffffffffu, n, src);
+      int src = __ffs(hit) - 1;
+      // Ranges far down a causal sequence see the most keys and go first: of one sequence
+      // among many, or, when a warp holds all sequences, of all of them, so that the last items
+      // to start are the short ones.
+      int place = __shfl_sync(0xffffffffu, n - 1 - (range - before - (incl - n)), src);
+      if (a.batch > 1 && a.batch <= 32) {
+        int level = n, count = 0, skipped = 0;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) level = max(level, __shfl_xor_sync(0xffffffffu, level, o));
+        unsigned has;
+        do {   // sequences that have a range at this place
+          has = __ballot_sync(0xffffffffu, n >= level);
+          skipped += count;
+          count = __popc(has);
+        } while (range >= skipped + count && --level > 0);
+        for (int i = range - skipped; i > 0; --i) has &= has - 1;
+        src = __ffs(has) - 1;
+        place = level - 1;
+      }
       q0 = __shfl_sync(0xffffffffu, q0, src);
       rows = __shfl_sync(0xffffffffu, rows, src);
       k0 = __shfl_sync(0xffffffffu, k0, src);
       keys = __shfl_sync(0xffffffffu, keys, src);
-      // the last ranges of a causal sequence see the most keys: they go first
-      const int r0 = (n - 1 - (range - first)) * a.tile_rows;
+      const int r0 = place * a.tile_rows;
       it.valid = 1;
       const bool two_heads = a.tile_rows == kRows;
       int last = 0;   // keys that any row sees
@@ -217,9 +232,9 @@ __host__ __device__ constexpr int partial_floats() {
 template <int kDim>
 struct Shape {
   static constexpr int kTile = kKeys * kDim * 2;         // bytes of 128 rows of a head
-  static constexpr int kRing = kDim == 128 ? 5 : 10;     // tiles of keys and values in flight
-  static constexpr int kSmem = 2 * kTile + kRing * kTile + 1024;
-  static constexpr int kPoly = kDim == 128 ? 2 : 0;      // pairs of eight whose exponentials go to the FMA pipe
+  static constexpr int kRing = kDim == 128 ? 4 : 10;     // tiles of keys and values in flight
+  static constexpr int kSmem = 2 * kTile + kRing * kTile + 8 * 4096 + 1024;   // and 32 rows of 64 outputs per warp
+  static constexpr int kPoly = kDim == 128 ? 2 : 3;      // pairs of eight whose exponentials go to the FMA pipe
   static constexpr int kO = 256;                         // tensor memory columns: S0, S1, O0, O1
 };
 
@@ -539,16 +554,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     int number = 0;
     while (true) {
       if (!mbar_wait_warp(&bar.item_full[slot.i], slot.phase, a.status, abort)) break;
-      const Item& sh = items[slot.i];
-      const int valid = sh.valid, keys = sh.keys, k0 = sh.k0, kvh = sh.kvh, n = sh.n[t], cut = sh.cut;
-      const int row0 = sh.row[t], rows = sh.rows[t], head = sh.head[t];
-      const int index = kShared ? sh.index : 0;
-      const int seen = a.causal ? min(keys, sh.seen[t] + row) : keys;   // keys of this row
-      const int all_see = min(keys, sh.seen[t]);
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bar.item_empty[slot.i]);
-      slot.next();
-      if (!valid) break;
+      // only what the loop needs is kept over it (its registers are full); the rest of the item
+      // is read behind it
+      const Item& it = items[slot.i];
+      if (!it.valid) break;
+      const int n = it.n[t];
+      const int seen = a.causal ? min(it.keys, it.seen[t] + row) : it.keys;   // keys of this row
+      const int all_see = min(it.keys, it.seen[t]);
       ++number;
       float m = -INFINITY;
       uint64_t sums[2] = {0, 0};   // two pairs of partial sums
@@ -664,6 +676,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(&bar.p_full[t][buf]);
       }
       if (!ok) break;
+      const int k0 = it.k0, kvh = it.kvh, cut = it.cut, row0 = it.row[t], rows = it.rows[t], head = it.head[t];
+      const int index = it.index;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar.item_empty[slot.i]);
+      slot.next();
       if (n >= 2) s_phase ^= 1u << (n & 1);   // what stood for the S after the last
       if (n > 0) {
         ok = mbar_wait_soon_warp(&bar.o_full[t], o_phase, a.status, abort);
@@ -684,8 +701,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         partial[(kDim + 1) * kRows] = l;
       }
       const bool extra = n > 0 && odd[number % (2 * kItems)] == number;
-      __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.out.data) +
-                           static_cast<long long>(row0 + row) * a.out.token_ld + head * a.out.head_ld;
+      __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.out.data) +   // of the warp's first row
+                           static_cast<long long>(row0 + (warp & 3) * 32) * a.out.token_ld + head * a.out.head_ld;
+      unsigned char* stage = ring + Sz::kRing * Sz::kTile + warp * 4096;
 #pragma unroll
       for (int c = 0; c < kDim / 32; ++c) {
         uint32_t o[32];
@@ -708,14 +726,27 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int i = 0; i < 32; ++i) partial[(c * 32 + i) * kRows] = n > 0 ? __uint_as_float(o[i]) : 0.0f;
           continue;
         }
+        // A lane has a row; stored from there, one instruction would touch 32 lines. 64 columns
+        // at a time go through shared memory, and 8 lanes store 128 bytes of a row.
+        unsigned char* mine = stage + lane * 128;
 #pragma unroll
-        for (int i = 0; i < 32; i += 8) {
+        for (int i = 0; i < 4; ++i) {
           uint32_t w[4];
 #pragma unroll
           for (int b = 0; b < 4; ++b)
-            w[b] = n > 0 ? pack_bf16(__uint_as_float(o[i + 2 * b]) * inv, __uint_as_float(o[i + 2 * b + 1]) * inv) : 0u;
-          if (row < rows && c * 32 + i < a.dim)
-            *reinterpret_cast<uint4*>(dst + c * 32 + i) = make_uint4(w[0], w[1], w[2], w[3]);
+            w[b] = n > 0 ? pack_bf16(__uint_as_float(o[8 * i + 2 * b]) * inv, __uint_as_float(o[8 * i + 2 * b + 1]) * inv)
+                         : 0u;
+          *reinterpret_cast<uint4*>(mine + ((((c & 1) * 4 + i) ^ (lane & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+        if ((c & 1) == 0) continue;
+        __syncwarp();
+        const int col = (c - 1) * 32 + (lane & 7) * 8;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int r = i * 4 + (lane >> 3);
+          const uint4 v = *reinterpret_cast<const uint4*>(stage + r * 128 + (((lane & 7) ^ (r & 7)) << 4));
+          if ((warp & 3) * 32 + r < rows && col < a.dim)
+            *reinterpret_cast<uint4*>(dst + r * a.out.token_ld + col) = v;
         }
       }
       tc_fence_before();
