@@ -150,10 +150,12 @@ def _heads(t: torch.Tensor, shape):
 
 
 def _out_heads(t: Optional[torch.Tensor], name: str, like: torch.Tensor, shape):
-    """(descriptor, tensor) of an output: the given one, or a dense new one."""
+    """(descriptor, tensor) of an output of the shape and type of `like`: the given one, or
+    a dense new one."""
     if t is None:
-        t = like.new_empty(shape)
-    elif t.shape != shape or t.dtype != like.dtype:
+        t = torch.empty_like(like, memory_format=torch.contiguous_format)
+        return SvdqHeads(t.data_ptr(), shape[1] * shape[2], shape[2], shape[1]), t
+    if t.shape != shape or t.dtype != like.dtype:
         raise ValueError(f"{name} must be {like.dtype} {tuple(shape)}")
     s, p = _layout(shape, t.stride(), t.element_size()), t.data_ptr()
     if s is None or p & 15:
@@ -171,32 +173,34 @@ def _shape3(t: torch.Tensor, name: str, dtype):
 
 
 def _vector(t, name: str, dtype, n: int):
-    if t.dtype != dtype or t.shape != (n,):
+    if t.dtype != dtype or t.numel() != n or t.dim() != 1:
         raise ValueError(f"{name} must be {dtype} [{n}]")
     return t if t.is_contiguous() else t.contiguous()
 
 
-def _ready(w):
-    """A norm weight, contiguous and on a 16-byte boundary."""
-    w = w.contiguous()
-    return w if not w.data_ptr() & 15 else w.clone()
+def _weight(w, dim: int):
+    """(norm weight, its type) as the library takes it."""
+    t = _TYPES.get(w.dtype)
+    if t is None or w.numel() != dim or w.dim() != 1:
+        raise ValueError(f"a norm weight must be bfloat16 or float32 [{dim}]")
+    if not w.is_contiguous() or w.data_ptr() & 15:
+        w = w.clone(memory_format=torch.contiguous_format)
+    return w, t
 
 
 def _weights(q_weight, k_weight, dim: int):
-    """(q_weight, k_weight, their pointers, their type) as the library takes them."""
-    dtype = None
-    for w in (q_weight, k_weight):
-        if w is None:
-            continue
-        if w.shape != (dim,):
-            raise ValueError(f"a norm weight must be [{dim}]")
-        if w.dtype not in _TYPES or (dtype is not None and w.dtype != dtype):
-            raise ValueError("the norm weights must have one type, bfloat16 or float32")
-        dtype = w.dtype
-    q_weight = None if q_weight is None else _ready(q_weight)
-    k_weight = None if k_weight is None else _ready(k_weight)
-    return (q_weight, k_weight, None if q_weight is None else q_weight.data_ptr(),
-            None if k_weight is None else k_weight.data_ptr(), SVDQ_BF16 if dtype is None else _TYPES[dtype])
+    """(the weights, their pointers, their type) as the library takes them."""
+    q_p = k_p = None
+    t = qt = kt = SVDQ_BF16
+    if q_weight is not None:
+        q_weight, qt = _weight(q_weight, dim)
+        q_p, t = q_weight.data_ptr(), qt
+    if k_weight is not None:
+        k_weight, kt = _weight(k_weight, dim)
+        k_p, t = k_weight.data_ptr(), kt
+        if q_p is not None and qt != kt:
+            raise ValueError("the norm weights must have one type")
+    return q_weight, k_weight, q_p, k_p, t
 
 
 def _rotation(rope: Optional[Rope], positions, tokens: int, dim: int):
@@ -263,7 +267,7 @@ def svdq_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, positions: Optional[torc
     qd, q = _heads(q, qs) if H else (_NO_HEADS, q)
     kd, k = _heads(k, ks) if ks[1] else (_NO_HEADS, k)
     qo, q_out = _out_heads(q_out, "q_out", q, qs) if H else (_NO_HEADS, q_out)
-    ko, k_out = _out_heads(k_out, "k_out", q, ks) if ks[1] else (_NO_HEADS, k_out)
+    ko, k_out = _out_heads(k_out, "k_out", k, ks) if ks[1] else (_NO_HEADS, k_out)
     st = load_library().svdq_qk_norm_rope(qd, kd, dt, T, D, pos, r, qw_p, kw_p, wdt, eps, qo, ko, _raw_stream(dev))
     if st:
         _check(st, "svdq_qk_norm_rope")

@@ -105,6 +105,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) heads_kernel(const __g
   __shared__ __align__(16) float sh_cos[kWarps][kMaxDim / 2], sh_sin[kWarps][kMaxDim / 2];
   __shared__ __align__(16) T sh_row[kPairing == kThroughShared ? kThreads * 2 * kVec : 1];
 
+  pdl_wait();
   const int warp = threadIdx.x / 32;
   const int lane = threadIdx.x % kLanes;                 // in the row
   const int group = threadIdx.x % 32 / kLanes;
@@ -404,14 +405,14 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) heads_kernel(const __g
 template <typename T, int kLanes, int kPairing>
 cudaError_t launch_pairing(const HeadsArgs& a, cudaStream_t st) {
   const int64_t warps = static_cast<int64_t>(kBlocksPerSm) * num_sms() * kWarps;
-  // A token's heads are divided only when there are fewer tokens than warps, down to one row
-  // per group: every share computes the cosines again (4 units per warp instead of one
-  // or two: 37 -> 57 us for an append of 6007 tokens).
+  // A token's heads are divided only as far as that leaves no warp a second unit, and down
+  // to one row per group: every share computes the cosines again, and a few units in a second
+  // turn double the time (1237 tokens in two shares: 12.3 us, whole 10.7).
   const int64_t most = ceil_div(std::max({a.q.heads, a.k.heads, 1}), 32 / kLanes);
-  const int64_t shares = std::max<int64_t>(1, std::min<int64_t>(most, ceil_div(warps, a.tokens)));
+  const int64_t shares = std::max<int64_t>(1, std::min<int64_t>(most, warps / a.tokens));
   const int64_t blocks = std::min<int64_t>(ceil_div(a.tokens * shares, kWarps), warps / kWarps);
-  heads_kernel<T, kLanes, kPairing><<<static_cast<unsigned>(blocks), kThreads, 0, st>>>(a, static_cast<int>(shares));
-  return cudaGetLastError();
+  return launch_behind(heads_kernel<T, kLanes, kPairing>, dim3(static_cast<unsigned>(blocks)), kThreads, 0, st, a,
+                       static_cast<int>(shares));
 }
 
 template <typename T, int kLanes>

@@ -6,6 +6,7 @@
 #include <cuda_runtime.h>
 #include <cstddef>
 #include <cstdint>
+#include <utility>
 
 #include "svdq.h"
 
@@ -135,6 +136,24 @@ cudaError_t launch_gemm_fp4(const svdq_weight* w, const uint8_t* act_codes,
                             void* split_ws = nullptr);
 
 // -------------------------------------------------- attention between linears
+// Launches `kernel` so that its blocks may start as those of the work queued before it end;
+// it must begin with griddepcontrol.wait (pdl_wait), before it touches memory.
+template <typename... Params, typename... Args>
+cudaError_t launch_behind(void (*kernel)(Params...), dim3 grid, int threads, size_t smem, cudaStream_t stream,
+                          Args&&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
+}
+
 // Norm and rotation of query and key heads (head_norm.cu). With a cache, rows of k
 // and v go to their slots too.
 struct HeadsArgs {

@@ -140,7 +140,7 @@ struct PagedShared {
 };
 
 template <int kDim, int kNt, int kStages>
-__global__ void __launch_bounds__(kThreads, kBlocksPerSm) paged_split_kernel(const PagedArgs a) {
+__global__ void __launch_bounds__(kThreads, kBlocksPerSm) paged_split_kernel(const __grid_constant__ PagedArgs a) {
   using Sh = PagedShared<kDim, kNt, kStages>;
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ unsigned sh_scan[2][kWarps];
@@ -149,6 +149,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) paged_split_kernel(con
   __shared__ float sh_m[kWarps][kRow * kNt], sh_l[kWarps][kRow * kNt];
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  pdl_wait();
   pdl_trigger();
 
   // this block's range [lo, hi) of the line of units, and the sequence it begins in; all
@@ -451,10 +452,11 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) paged_split_kernel(con
 }
 
 // Joins the pieces of one segment's row: grid (batch * segments, rows of a segment).
+constexpr int kJoinThreads = 256;
 template <int kDim, int kNt>
-__global__ void __launch_bounds__(kThreads) paged_join_kernel(const PagedArgs a) {
-  constexpr int kShares = kThreads / kDim;   // threads per element: each takes every kShares-th piece
-  __shared__ float sh_red[kWarps];
+__global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_constant__ PagedArgs a) {
+  constexpr int kShares = kJoinThreads / kDim;   // threads per element: each takes every kShares-th piece
+  __shared__ float sh_red[2][kJoinThreads / 32];
   __shared__ float sh_weight[kMaxRanges];
   __shared__ float sh_sum[kShares][kDim];
   const int tid = threadIdx.x;
@@ -480,34 +482,43 @@ __global__ void __launch_bounds__(kThreads) paged_join_kernel(const PagedArgs a)
     return mine + static_cast<long long>(i) * step + (i == 0 ? slot0 * partial_floats<kDim, kNt>() : 0);
   };
   // all maxima and totals at once, then the weighted sums in independent loads
-  float top = -INFINITY;
-  for (int i = tid; i < pieces; i += kThreads) {
-    sh_weight[i] = piece(i)[kRow * kNt * kDim + blockIdx.y];
-    top = fmaxf(top, sh_weight[i]);
+  constexpr int kMine = (kMaxRanges + kJoinThreads - 1) / kJoinThreads;
+  float top = -INFINITY, tot = 0.0f, m[kMine], l[kMine];
+#pragma unroll
+  for (int j = 0; j < kMine; ++j) {
+    const int i = tid + j * kJoinThreads;
+    m[j] = -INFINITY, l[j] = 0.0f;
+    if (i < pieces) {
+      m[j] = piece(i)[kRow * kNt * kDim + blockIdx.y];
+      l[j] = piece(i)[kRow * kNt * (kDim + 1) + blockIdx.y];
+    }
+    top = fmaxf(top, m[j]);
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-  if ((tid & 31) == 0) sh_red[tid >> 5] = top;
+  if ((tid & 31) == 0) sh_red[0][tid >> 5] = top;
   __syncthreads();
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) top = fmaxf(top, sh_red[w]);
-  __syncthreads();
-  float tot = 0.0f;
-  for (int i = tid; i < pieces; i += kThreads) {
-    const float f = exp2_from(sh_weight[i], top);
-    sh_weight[i] = f;
-    tot = fmaf(f, piece(i)[kRow * kNt * (kDim + 1) + blockIdx.y], tot);
+  for (int w = 0; w < kJoinThreads / 32; ++w) top = fmaxf(top, sh_red[0][w]);
+#pragma unroll
+  for (int j = 0; j < kMine; ++j) {
+    const int i = tid + j * kJoinThreads;
+    const float f = exp2_from(m[j], top);
+    if (i < pieces) sh_weight[i] = f;
+    tot = fmaf(f, l[j], tot);
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) tot += __shfl_xor_sync(0xffffffffu, tot, o);
-  if ((tid & 31) == 0) sh_red[tid >> 5] = tot;
+  if ((tid & 31) == 0) sh_red[1][tid >> 5] = tot;
   __syncthreads();
   tot = 0.0f;
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) tot += sh_red[w];
+  for (int w = 0; w < kJoinThreads / 32; ++w) tot += sh_red[1][w];
   float sum = 0.0f;
-#pragma unroll 8
-  for (int i = share; i < pieces; i += kShares) sum = fmaf(sh_weight[i], d < a.cache.head_dim ? piece(i)[blockIdx.y * kDim + d] : 0.0f, sum);
+  if (d < a.cache.head_dim) {
+#pragma unroll 10
+    for (int i = share; i < pieces; i += kShares) sum = fmaf(sh_weight[i], piece(i)[blockIdx.y * kDim + d], sum);
+  }
   sh_sum[share][d] = sum;
   __syncthreads();
   if (!writes) return;
@@ -528,20 +539,11 @@ cudaError_t launch_one(PagedArgs a, cudaStream_t st) {
   cudaError_t e = cudaFuncSetAttribute(paged_split_kernel<kDim, kNt, kStages>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  paged_split_kernel<kDim, kNt, kStages><<<a.grid * a.abreast, kThreads, smem, st>>>(a);
-  e = cudaGetLastError();
+  e = launch_behind(paged_split_kernel<kDim, kNt, kStages>, dim3(a.grid * a.abreast), kThreads, smem, st, a);
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(a.batch) * a.cache.heads * a.row_groups,
-                     static_cast<unsigned>(std::min(a.group, kRow * kNt)));
-  cfg.blockDim = dim3(kThreads);
-  cfg.stream = st;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, paged_join_kernel<kDim, kNt>, a);
+  const dim3 rows(static_cast<unsigned>(a.batch) * a.cache.heads * a.row_groups,
+                  static_cast<unsigned>(std::min(a.group, kRow * kNt)));
+  return launch_behind(paged_join_kernel<kDim, kNt>, rows, kJoinThreads, 0, st, a);
 }
 
 }  // namespace

@@ -833,16 +833,7 @@ cudaError_t launch_dim(const PromptArgs& a, const CUtensorMap& mq, const CUtenso
   kernel<<<static_cast<unsigned>(items * a.shares), kThreads, smem, st>>>(mq, mk, mv, a);
   e = cudaGetLastError();
   if (e != cudaSuccess || a.shares == 1) return e;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(items), 2, 4);
-  cfg.blockDim = dim3(kJoinThreads);
-  cfg.stream = st;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, prompt_join_kernel<kDim>, a);
+  return launch_behind(prompt_join_kernel<kDim>, dim3(static_cast<unsigned>(items), 2, 4), kJoinThreads, 0, st, a);
 }
 
 }  // namespace
