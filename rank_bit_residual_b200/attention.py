@@ -86,8 +86,28 @@ _NO_HEADS = SvdqHeads(None, 0, 0, 0)
 _NO_ROPE = SvdqRope(None, 0, 0, 1.0)
 
 # A decode step calls these functions between kernels of a few microseconds, so their host
-# work counts: what depends on a layout alone is kept by layout (shape, strides, type),
-# pointers go to ctypes as plain ints, and each tensor is asked for a property once.
+# work counts. The usual call goes through _calls.so (csrc/attention_calls.cpp), which reads
+# the tensors directly: 5 us. What it does not take - a copy to make, another device than the
+# current one, a mistake to name - comes back as None and goes the long way below: 15 us.
+
+_calls = None
+_calls_lib = None
+
+
+def _quick():
+    """The module of quick calls, bound to the loaded library."""
+    global _calls, _calls_lib
+    lib = load_library()
+    if _calls_lib is not lib:
+        try:
+            from . import _calls as module
+        except ImportError as e:
+            raise ImportError("_calls.so not built; run python -m rank_bit_residual_b200.build") from e
+        module.bind(*(ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in (
+            "svdq_qk_norm_rope", "svdq_kv_append", "svdq_attention_prompt", "svdq_attention_prompt_workspace_size",
+            "svdq_attention_decode", "svdq_attention_decode_workspace_size")))
+        _calls, _calls_lib = module, lib
+    return _calls
 
 
 def _device(first, *others) -> int:
@@ -238,7 +258,6 @@ def _cache(k_cache, v_cache):
     return SvdqKvCache(k, v, shape[0], s[0], s[1], s[2], shape[1], shape[2], shape[3])
 
 
-@_on_device
 def svdq_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, positions: Optional[torch.Tensor] = None,
                       rope: Optional[Rope] = None, q_weight: Optional[torch.Tensor] = None,
                       k_weight: Optional[torch.Tensor] = None, eps: float = 1e-6,
@@ -249,6 +268,15 @@ def svdq_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, positions: Optional[torc
     q [T, H, D], k [T, Hkv, D], bf16 or fp32; positions int64 [T]; weights [D] bf16 or
     fp32. q_out=q, k_out=k work in place. Returns (q_out, k_out).
     """
+    turns, inter, amp = (None, False, 1.0) if rope is None else (rope.turns, rope.interleaved, rope.amplitude)
+    done = _quick().norm_rope(q, k, positions, turns, inter, amp, q_weight, k_weight, eps, q_out, k_out)
+    if done is not None:
+        return done
+    return _qk_norm_rope(q, k, positions, rope, q_weight, k_weight, eps, q_out, k_out)
+
+
+@_on_device
+def _qk_norm_rope(q, k, positions, rope, q_weight, k_weight, eps, q_out, k_out):
     dev = _device(q, k, positions, q_weight, k_weight, q_out, k_out, None if rope is None else rope.turns)
     dt = _TYPES.get(q.dtype)
     if dt is None:
@@ -274,7 +302,6 @@ def svdq_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, positions: Optional[torc
     return q_out, k_out
 
 
-@_on_device
 def svdq_kv_append(k_cache: torch.Tensor, v_cache: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
                    slots: torch.Tensor, positions: Optional[torch.Tensor] = None, rope: Optional[Rope] = None,
                    k_weight: Optional[torch.Tensor] = None, eps: float = 1e-6, q: Optional[torch.Tensor] = None,
@@ -287,6 +314,17 @@ def svdq_kv_append(k_cache: torch.Tensor, v_cache: torch.Tensor, k: torch.Tensor
     twice. q [T, H, D] is normed and rotated in the same pass. k_out receives the
     finished keys too (k_out=k: in place). Returns q_out (None without q).
     """
+    if q is not None:
+        turns, inter, amp = (None, False, 1.0) if rope is None else (rope.turns, rope.interleaved, rope.amplitude)
+        done = _quick().append(k_cache, v_cache, k, v, slots, positions, turns, inter, amp, k_weight, eps, q, q_weight,
+                               q_out, k_out)
+        if done is not None:
+            return done
+    return _kv_append(k_cache, v_cache, k, v, slots, positions, rope, k_weight, eps, q, q_weight, q_out, k_out)
+
+
+@_on_device
+def _kv_append(k_cache, v_cache, k, v, slots, positions, rope, k_weight, eps, q, q_weight, q_out, k_out):
     dev = _device(k_cache, v_cache, k, v, slots, positions, k_weight, q, q_weight, q_out, k_out,
                   None if rope is None else rope.turns)
     c = _cache(k_cache, v_cache)
@@ -330,7 +368,6 @@ def _prompt_scratch(dev: int, heads: int, kv_heads: int, dim: int, batch: int, q
     return size.value
 
 
-@_on_device
 def svdq_attention_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: Optional[torch.Tensor] = None,
                           cu_k: Optional[torch.Tensor] = None, causal: bool = True,
                           scale: Optional[float] = None, out: Optional[torch.Tensor] = None,
@@ -344,6 +381,15 @@ def svdq_attention_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_
     Scratch (few rows over many keys need some) is allocated per call unless a workspace
     is given (one per stream in flight). Returns [Tq, H, D].
     """
+    if workspace is None:
+        done = _quick().prompt(q, k, v, cu_q, cu_k, causal, scale, out)
+        if done is not None:
+            return done
+    return _attention_prompt(q, k, v, cu_q, cu_k, causal, scale, out, workspace)
+
+
+@_on_device
+def _attention_prompt(q, k, v, cu_q, cu_k, causal, scale, out, workspace):
     dev = _device(q, k, v, cu_q, cu_k, out)
     qs, ks, vs = _shape3(q, "q", _BF16), _shape3(k, "k", _BF16), _shape3(v, "v", _BF16)
     T, H, D = qs
@@ -389,7 +435,6 @@ def _decode_scratch(dev: int, batch: int, heads: int, kv_heads: int, dim: int) -
     return size.value
 
 
-@_on_device
 def svdq_attention_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, page_table: torch.Tensor,
                           kv_len: torch.Tensor, scale: Optional[float] = None, out: Optional[torch.Tensor] = None,
                           workspace: Optional[LinearWorkspace] = None) -> torch.Tensor:
@@ -399,6 +444,15 @@ def svdq_attention_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch
     [B] (0: a zero row). The scratch is allocated per call unless a workspace is given
     (one per stream in flight). Returns [B, H, D].
     """
+    if workspace is None:
+        done = _quick().decode(q, k_cache, v_cache, page_table, kv_len, scale, out)
+        if done is not None:
+            return done
+    return _attention_decode(q, k_cache, v_cache, page_table, kv_len, scale, out, workspace)
+
+
+@_on_device
+def _attention_decode(q, k_cache, v_cache, page_table, kv_len, scale, out, workspace):
     dev = _device(q, k_cache, v_cache, page_table, kv_len, out)
     c = _cache(k_cache, v_cache)
     qs = _shape3(q, "q", _BF16)

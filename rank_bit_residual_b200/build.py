@@ -5,7 +5,9 @@
 Each csrc/*.cu file is compiled separately (in parallel) into _build/ and the
 objects are linked into rank_bit_residual_b200/libsvdq.so. The CUDA runtime is
 linked statically; the driver API is reached through cudaGetDriverEntryPoint,
-so loading the library needs no libcuda at link time.
+so loading the library needs no libcuda at link time. csrc/attention_calls.cpp, the
+quick calls of the attention operators, is compiled against torch and Python with the host
+compiler and becomes rank_bit_residual_b200/_calls.so.
 """
 
 from __future__ import annotations
@@ -15,12 +17,15 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libsvdq.so")
+CALLS_SRC = os.path.join(CSRC, "attention_calls.cpp")
+CALLS = os.path.join(PKG, "_calls.so")
 INCLUDE = os.path.join(ROOT, "include")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
@@ -51,15 +56,38 @@ def up_to_date() -> bool:
     return all(os.path.getmtime(d) <= t for d in _deps())
 
 
+def calls_up_to_date() -> bool:
+    deps = [CALLS_SRC] + glob.glob(os.path.join(INCLUDE, "*.h"))
+    return os.path.exists(CALLS) and all(os.path.getmtime(d) <= os.path.getmtime(CALLS) for d in deps)
+
+
+def calls_command(out: str):
+    """The host compiler's command line for the quick calls."""
+    import torch
+    root = os.path.dirname(torch.__file__)
+    inc = os.path.join(root, "include")
+    lib = os.path.join(root, "lib")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")
+    return ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-w",
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+            "-I" + INCLUDE, "-isystem", inc, "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"),
+            "-isystem", cuda, "-isystem", sysconfig.get_paths()["include"], CALLS_SRC, "-o", out,
+            "-L" + lib, "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
     """Compile and link; returns the library path. Raises on any compiler error."""
-    if not force and up_to_date():
-        return LIB
+    procs = []
+    calls = None
+    if force or not calls_up_to_date():
+        calls = CALLS + ".tmp"
+        procs.append((CALLS_SRC, subprocess.Popen(calls_command(calls), stdout=subprocess.PIPE,
+                                                  stderr=subprocess.STDOUT)))
+    build_lib = force or not up_to_date()
     os.makedirs(BUILD, exist_ok=True)
     cc = nvcc()
-    procs = []
     objs = []
-    for src in sources():
+    for src in sources() if build_lib else ():
         obj = os.path.join(BUILD, os.path.basename(src)[:-3] + ".o")
         objs.append(obj)
         cmd = [cc, *ARCH, *FLAGS, "-c", src, "-o", obj]
@@ -75,7 +103,11 @@ def build(force: bool = False, verbose: bool = False) -> str:
             print(out.decode(errors="replace"))
     if failed:
         msg = "\n".join(f"--- {s}\n{o}" for s, o in failed)
-        raise RuntimeError(f"nvcc failed:\n{msg}")
+        raise RuntimeError(f"the compiler failed:\n{msg}")
+    if calls:
+        os.replace(calls, CALLS)
+    if not build_lib:
+        return LIB
     tmp = LIB + ".tmp"
     cmd = [cc, *ARCH, "-shared", "-Xcompiler", "-fPIC", "-o", tmp, *objs]
     r = subprocess.run(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)

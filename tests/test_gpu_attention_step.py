@@ -6,6 +6,7 @@ import pytest
 import torch
 
 import rank_bit_residual_b200 as rb
+import rank_bit_residual_b200.attention as rba
 from oracle import attention as oa
 from tests.gpu_util import SyntheticWeight, device
 
@@ -161,6 +162,65 @@ def test_decode_steps_in_a_graph():
         assert torch.equal(y, want[i]), i
     assert rb.svdq_check_status() == rb.SVDQ_OK
     assert torch.equal(caches[0][0], caches[1][0]) and torch.equal(caches[0][1], caches[1][1])
+
+
+def test_the_quick_and_the_long_way_agree():
+    """The binding's quick calls and the checked ones behind them, on the same arguments."""
+    T = 40
+    row = draw(1, T, (H + 2 * K) * D)
+    q, k, v = row.view(T, -1, D).split([H, K, K], 1)
+    pos, st = torch.arange(T, device=device()), settings()
+    args = (pos, st["rope"], st["q_weight"], st["k_weight"], 1e-6)
+    quick, calls = rba._quick(), []
+
+    class Spy:
+        def __getattr__(self, name):
+            def call(*a):
+                calls.append((name, getattr(quick, name)(*a)))
+                return calls[-1][1]
+            return call
+
+    saved = rba._calls
+    rba._calls = Spy()
+    try:
+        a = rb.svdq_qk_norm_rope(q, k, *args)
+        kc, vc = paged(4)
+        slots = torch.arange(T, device=device())
+        qa = rb.svdq_kv_append(kc, vc, k, v, slots, pos, st["rope"], st["k_weight"], q=q, q_weight=st["q_weight"])
+        cu = ints([0, 13, T])
+        o = rb.svdq_attention_prompt(a[0], a[1], v, cu, cu)
+        table, lens = ints([[0, 1, 2]]), ints([T])
+        d = rb.svdq_attention_decode(a[0][:1], kc, vc, table, lens)
+    finally:
+        rba._calls = saved
+    assert [n for n, _ in calls] == ["norm_rope", "append", "prompt", "decode"]
+    assert all(r is not None for _, r in calls)                 # none of them was sent the long way
+    b = rba._qk_norm_rope(q, k, *args, None, None)
+    kc2, vc2 = paged(4)
+    qb = rba._kv_append(kc2, vc2, k, v, slots, pos, st["rope"], st["k_weight"], 1e-6, q, st["q_weight"], None, None)
+    ob = rba._attention_prompt(a[0], a[1], v, cu, cu, True, None, None, None)
+    db = rba._attention_decode(a[0][:1], kc2, vc2, table, lens, None, None, None)
+    for x, y in ((a[0], b[0]), (a[1], b[1]), (qa, qb), (kc, kc2), (vc, vc2), (o, ob), (d, db)):
+        assert torch.equal(x, y) and x.stride() == y.stride()
+
+
+def test_quick_calls_send_the_unusual_on():
+    """What needs a copy or a message is not taken, and nothing is launched for it."""
+    quick = rba._quick()
+    q, k = draw(1, 4, H, D), draw(2, 4, K, D)
+    pos, turns = torch.arange(4, device=device()), rb.Rope.make(D).turns
+    usual = dict(q=q, k=k, positions=pos, turns=turns, inter=False, amp=1.0, qw=None, kw=None, eps=1e-6, qo=None, ko=None)
+    assert quick.norm_rope(*usual.values()) is not None
+    flat = torch.empty(4 * H * D + 1, dtype=torch.bfloat16, device=device())
+    for change in (dict(q=q.half()), dict(q=q.float()), dict(q=q.cpu()), dict(q=q[0]), dict(q=flat[1:].view(4, H, D)),
+                   dict(q=q[:, :, ::2]), dict(k=k[:3]), dict(positions=None), dict(positions=pos.int()),
+                   dict(positions=pos[:3]), dict(turns=turns.float()), dict(turns=torch.cat([turns, turns])),
+                   dict(amp="x"), dict(eps=None), dict(eps=-1.0), dict(qw=draw(3, 8)), dict(qw=draw(3, D).half()),
+                   dict(qw=draw(3, D), kw=draw(3, D).float()), dict(qo=k), dict(ko=k.float()), dict(q=None), dict(q=1),
+                   dict(q=q[:0], k=k[:0], positions=pos[:0]), dict(q=q[:, :0])):
+        assert quick.norm_rope(*{**usual, **change}.values()) is None, change
+    assert quick.norm_rope(q, k) is None and quick.decode(q) is None
+    assert rb.svdq_check_status() == rb.SVDQ_OK
 
 
 def test_two_graphs_replayed_on_two_streams():
