@@ -487,7 +487,7 @@ svdq_status svdq_kv_append(const svdq_kv_cache* cache, svdq_heads k, svdq_heads 
  *              read or written then, but the rows of the call have no meaning.
  *   causal     1: row i of a sequence of n rows and m keys sees keys 0 .. m - n + i
  *              (rows and keys end together); 0: all keys
- *   scale      finite, e.g. 1 / sqrt(head_dim)
+ *   scale      below 2^126 in magnitude, e.g. 1 / sqrt(head_dim)
  *   out        [q_tokens, heads, head_dim], must not overlap an input. A row that sees
  *              no key becomes zero. Rows of no sequence are left as they were.
  *   workspace  svdq_attention_prompt_workspace_size bytes (16-byte aligned; 0 bytes, and

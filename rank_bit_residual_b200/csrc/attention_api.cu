@@ -13,6 +13,7 @@ namespace {
 constexpr int64_t kMaxTokens = int64_t(1) << 30;   // of the norm and the append
 constexpr int64_t kMaxPrompt = int64_t(1) << 24;   // rows, keys, sequences and heads of attention
 constexpr int kMaxHeads = 1 << 15;
+constexpr float kMaxScale = 8.507059e37f;   // 2^126: times log2(e) it is still finite
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
@@ -162,7 +163,7 @@ svdq_status svdq_attention_prompt(svdq_heads q, svdq_heads k, svdq_heads v, cons
                                   const int32_t* cu_k, int32_t batch, int64_t q_tokens, int64_t k_tokens,
                                   int32_t head_dim, int32_t causal, float scale, svdq_heads out,
                                   void* workspace, size_t workspace_bytes, svdq_stream_t stream) {
-  if ((causal != 0 && causal != 1) || !std::isfinite(scale)) return SVDQ_EINVAL;
+  if ((causal != 0 && causal != 1) || !(std::fabs(scale) < kMaxScale)) return SVDQ_EINVAL;
   svdq_status s = check_prompt_sizes(q.heads, k.heads, head_dim, batch, q_tokens, k_tokens);
   if (s != SVDQ_OK) return s;
   if (batch == 0 || q_tokens == 0) return SVDQ_OK;
@@ -199,7 +200,7 @@ svdq_status svdq_attention_decode(svdq_heads q, const svdq_kv_cache* cache, cons
                                   svdq_stream_t stream) {
   svdq_status s = check_cache(cache, 128);
   if (s != SVDQ_OK) return s;
-  if (!std::isfinite(scale) || table_ld < 0) return SVDQ_EINVAL;
+  if (!(std::fabs(scale) < kMaxScale) || table_ld < 0) return SVDQ_EINVAL;
   if ((s = check_decode_sizes(batch, q.heads, cache->heads, cache->head_dim)) != SVDQ_OK) return s;
   if (batch == 0) return SVDQ_OK;
   if (!kv_len || (!page_table && table_ld > 0) || absent(q)) return SVDQ_EINVAL;

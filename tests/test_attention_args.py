@@ -111,7 +111,7 @@ def prompt(lib, q=None, k=None, v=None, cu_q=P, cu_k=P, batch=2, q_tokens=5, k_t
 
 @pytest.mark.parametrize("kw", [
     dict(batch=-1), dict(q_tokens=-1), dict(k_tokens=-1), dict(causal=2), dict(scale=float("nan")),
-    dict(scale=float("inf")), dict(cu_q=None), dict(cu_k=None), dict(q=NONE), dict(q=heads(3)), dict(v=heads(4)),
+    dict(scale=float("inf")), dict(scale=3e38), dict(cu_q=None), dict(cu_k=None), dict(q=NONE), dict(q=heads(3)), dict(v=heads(4)),
     dict(k=heads(2, data=None)), dict(k=heads(0), v=heads(0)), dict(out=heads()), dict(out=heads(2, data=2 * P)),
     dict(dim=0),
 ])
@@ -154,7 +154,7 @@ def decode(lib, q=None, c=None, table=P, table_ld=4, kv_len=P, batch=3, scale=0.
 
 @pytest.mark.parametrize("kw", [
     dict(c="none"), dict(c=cache(pages=0)), dict(q=heads(3)), dict(q=NONE), dict(table=None), dict(table_ld=-1),
-    dict(kv_len=None), dict(batch=-1), dict(scale=float("nan")), dict(out=heads()), dict(out=heads(2, data=2 * P)),
+    dict(kv_len=None), dict(batch=-1), dict(scale=float("nan")), dict(scale=-3e38), dict(out=heads()), dict(out=heads(2, data=2 * P)),
 ])
 def test_decode_invalid(lib, kw):
     assert decode(lib, **kw) == rb.SVDQ_EINVAL

@@ -223,6 +223,80 @@ def test_quick_calls_send_the_unusual_on():
     assert rb.svdq_check_status() == rb.SVDQ_OK
 
 
+def test_captured_behind_a_memset_a_copy_and_two_streams():
+    """The kernels start behind the work before them: also where that is no kernel, or is
+    on two streams."""
+    T = 64
+    src = draw(1, T, (H + 2 * K) * D)
+    row = torch.zeros_like(src)
+    q, k, v = row.view(T, -1, D).split([H, K, K], 1)
+    pos = torch.arange(T, device=device())
+    rope = rb.Rope.make(D)
+    kc, vc = paged(8)
+    table, lens = ints([[0, 1, 2, 3]]), ints([T])
+
+    def work():
+        a, b = rb.svdq_qk_norm_rope(q, k, pos, rope)
+        rb.svdq_kv_append(kc, vc, b, v, pos, q=a, k_out=b)
+        return rb.svdq_attention_prompt(a, b, v), rb.svdq_attention_decode(a[-1:], kc, vc, table, lens)
+
+    row.copy_(src)
+    want = [t.clone() for t in work()]
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for kind in ("copy", "memset", "streams"):
+        row.zero_(), kc.zero_(), vc.zero_()
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            if kind == "streams":
+                side.wait_stream(torch.cuda.current_stream())
+                with torch.cuda.stream(side):
+                    row[T // 2:].copy_(src[T // 2:])
+                row[:T // 2].copy_(src[:T // 2])
+                torch.cuda.current_stream().wait_stream(side)
+            else:
+                row.copy_(src)
+                if kind == "memset":
+                    kc.zero_()
+            got = work()
+        for _ in range(3):
+            g.replay()
+        torch.cuda.synchronize()
+        for x, y in zip(got, want):
+            assert torch.equal(x, y), kind
+    assert rb.svdq_check_status() == rb.SVDQ_OK
+
+
+def test_calls_of_two_threads():
+    """Two host threads, each on its own stream."""
+    import threading
+    kc, vc = draw(1, 300, PAGE, K, D), draw(2, 300, PAGE, K, D)
+    table, lens = ints(np.arange(300, dtype=np.int32).reshape(2, 150)), ints([2400, 2001])
+    qs = [draw(3, 2, H, D), draw(4, 2, H, D)]
+    row = draw(5, 300, (H + 2 * K) * D)
+    pq, pk, pv = row.view(300, -1, D).split([H, K, K], 1)
+    want = [rb.svdq_attention_decode(q, kc, vc, table, lens) for q in qs]
+    prompt = rb.svdq_attention_prompt(pq, pk, pv)
+    torch.cuda.synchronize()
+    bad = []
+
+    def run(i):
+        with torch.cuda.stream(torch.cuda.Stream()):
+            for _ in range(50):
+                if not torch.equal(rb.svdq_attention_decode(qs[i], kc, vc, table, lens), want[i]):
+                    bad.append(("decode", i))
+                if not torch.equal(rb.svdq_attention_prompt(pq, pk, pv), prompt):
+                    bad.append(("prompt", i))
+
+    threads = [threading.Thread(target=run, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not bad and rb.svdq_check_status() == rb.SVDQ_OK
+
+
 def test_two_graphs_replayed_on_two_streams():
     """Each captured decode call has its own scratch: replays may overlap."""
     kc, vc = draw(1, 600, PAGE, K, D), draw(2, 600, PAGE, K, D)
