@@ -28,7 +28,7 @@
 //
 // Few rows over many keys would leave most SMs idle: the keys of an item are then divided
 // among several items, whose unfinished sums a second kernel joins (301 rows over 7501 keys,
-// 48 items: 108 -> 68 us with three shares).
+// 48 items: 108 us with one share, 63 with three).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -88,18 +88,28 @@ __device__ __forceinline__ bool bad_cu(const int32_t* cu, int s, long long token
   return cu && (cu[s] < 0 || cu[s + 1] < cu[s] || cu[s + 1] > tokens);
 }
 
+// Sequences that a warp has walked past, and their row ranges.
+struct Walked {
+  int sequences = 0, ranges = 0;
+};
+
 // Item `index` of the line: row ranges of all sequences, each with its `pairs` heads. The
-// whole warp calls it; valid = 0 past the last range.
-__device__ Item find_item(const PromptArgs& a, int index) {
+// whole warp calls it; valid = 0 past the last range. A block's items come in order, so the walk
+// goes on from where the last one ended (from the start each time, 6000 sequences of 7 rows
+// took @OLD@ us instead of @NEW@).
+__device__ Item find_item(const PromptArgs& a, int index, Walked& w) {
   const int lane = threadIdx.x & 31;
+  // every index of the grid passes here, and there are at least as many as sequences
+  if (index < a.batch && lane == 0 && (bad_cu(a.cu_q, index, a.q_tokens) || bad_cu(a.cu_k, index, a.k_tokens)))
+    record_status(a.status, kStatusEinval);
   const int whole = index / a.shares, part = index - whole * a.shares;
   const int range = whole / a.pairs, pair = whole - range * a.pairs;
   Item it;
   it.valid = 0;
   it.index = index;
-  int before = 0;
-  for (int s0 = 0; s0 < a.batch; s0 += 32) {
-    const int s = s0 + lane;
+  if (range < w.ranges) w = Walked();
+  for (; w.sequences < a.batch; w.sequences += 32) {
+    const int before = w.ranges, s = w.sequences + lane;
     int n = 0, q0 = 0, rows = 0, k0 = 0, keys = 0;
     if (s < a.batch) {
       q0 = static_cast<int>(cu_at(a.cu_q, s, a.q_tokens));
@@ -107,8 +117,6 @@ __device__ Item find_item(const PromptArgs& a, int index) {
       k0 = static_cast<int>(cu_at(a.cu_k, s, a.k_tokens));
       keys = max(0, static_cast<int>(cu_at(a.cu_k, s + 1, a.k_tokens)) - k0);
       n = (rows + a.tile_rows - 1) / a.tile_rows;
-      if (index == 0 && (bad_cu(a.cu_q, s, a.q_tokens) || bad_cu(a.cu_k, s, a.k_tokens)))
-        record_status(a.status, kStatusEinval);
     }
     int incl = n;
 #pragma unroll
@@ -124,18 +132,20 @@ __device__ Item find_item(const PromptArgs& a, int index) {
       // to start are the short ones.
       int place = __shfl_sync(0xffffffffu, n - 1 - (range - before - (incl - n)), src);
       if (a.batch > 1 && a.batch <= 32) {
-        int level = n, count = 0, skipped = 0;
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) level = max(level, __shfl_xor_sync(0xffffffffu, level, o));
-        unsigned has;
-        do {   // sequences that have a range at this place
-          has = __ballot_sync(0xffffffffu, n >= level);
-          skipped += count;
-          count = __popc(has);
-        } while (range >= skipped + count && --level > 0);
+        // the farthest place with more than `range` ranges at it or behind it
+        int end = __reduce_max_sync(0xffffffffu, n), skipped = 0;   // ranges at `end` or behind it
+        place = 0;
+        while (end - place > 1) {
+          const int middle = (place + end) / 2;
+          const int behind = __reduce_add_sync(0xffffffffu, max(0, n - middle));
+          if (behind > range)
+            place = middle;
+          else
+            end = middle, skipped = behind;
+        }
+        unsigned has = __ballot_sync(0xffffffffu, n > place);   // sequences that reach this place
         for (int i = range - skipped; i > 0; --i) has &= has - 1;
         src = __ffs(has) - 1;
-        place = level - 1;
       }
       q0 = __shfl_sync(0xffffffffu, q0, src);
       rows = __shfl_sync(0xffffffffu, rows, src);
@@ -172,7 +182,7 @@ __device__ Item find_item(const PromptArgs& a, int index) {
       it.kvh = it.head[0] / (a.q.heads / a.k.heads);
       return it;
     }
-    before += __shfl_sync(0xffffffffu, incl, 31);
+    w.ranges += __shfl_sync(0xffffffffu, incl, 31);
   }
   return it;
 }
@@ -321,6 +331,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       Turn<Sz::kRing> r;
       uint32_t q_phase = 0, answer_phase = 0, last_raw = 0, raw_phase = 0;   // the last two by ring position
       int index = blockIdx.x;
+      Walked walked;
       bool ok = true;
       while (ok) {
         // ask for the next item while this one is worked on
@@ -330,7 +341,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         Item it;
         it.valid = 0;
-        if (index >= 0) it = find_item(a, index);
+        if (index >= 0) it = find_item(a, index, walked);
         if (index < 0 || it.valid) {
           ok = mbar_wait_warp(&bar.item_empty[slot.i], slot.phase ^ 1, a.status, abort);
           if (ok && lane == 0) {
@@ -767,7 +778,8 @@ template <int kDim>
 __global__ void __launch_bounds__(kJoinThreads) prompt_join_kernel(const __grid_constant__ PromptArgs a) {
   __shared__ Item sh_item;
   if (threadIdx.x < 32) {
-    const Item it = find_item(a, blockIdx.x * a.shares);
+    Walked from_start;
+    const Item it = find_item(a, blockIdx.x * a.shares, from_start);
     if (threadIdx.x == 0) sh_item = it;
   }
   __syncthreads();

@@ -178,6 +178,31 @@ def test_prompt_bad_lists_are_recorded():
     assert rb.svdq_check_status() == rb.SVDQ_OK
 
 
+@pytest.mark.parametrize("place", [31, 32, 69])
+def test_prompt_bad_lists_are_recorded_in_long_batches(place):
+    cu = [2 * i for i in range(71)]
+    q, k, v = draw(1, 140, 2, 64), draw(2, 140, 1, 64), draw(3, 140, 1, 64)
+    good = rb.svdq_attention_prompt(q, k, v, ints(cu), ints(cu))
+    assert rb.svdq_check_status() == rb.SVDQ_OK
+    cu[place] += 3                           # beyond the next one
+    for lists in ((cu, [2 * i for i in range(71)]), ([2 * i for i in range(71)], cu)):
+        got = rb.svdq_attention_prompt(q, k, v, *map(ints, lists))
+        assert rb.svdq_check_status() == rb.SVDQ_EINVAL
+        assert torch.equal(got[:2 * place - 2], good[:2 * place - 2])
+
+
+@pytest.mark.parametrize("lens", [[1, 700, 129, 0, 384, 385], [260] * 5, [1] * 31 + [2000], [0] * 40 + [300, 0, 9]])
+@pytest.mark.parametrize("heads, kv_heads", [(4, 2), (3, 1)])
+def test_prompt_every_range_of_every_sequence_has_its_turn(lens, heads, kv_heads):
+    """One key per sequence: each row is a copy of its sequence's value."""
+    n, total = len(lens), sum(lens)
+    q, k, v = draw(1, total, heads, 64), draw(2, n, kv_heads, 64), draw(3, n, kv_heads, 64)
+    cu = [sum(lens[:i]) for i in range(n + 1)]
+    got = rb.svdq_attention_prompt(q, k, v, ints(cu), ints(range(n + 1)), causal=False)
+    of = torch.repeat_interleave(torch.arange(n), torch.tensor(lens)).to(got.device)
+    assert torch.equal(got, v[of].repeat_interleave(heads // kv_heads, 1))
+
+
 def test_prompt_no_keys_and_no_rows():
     q = draw(1, 40, 2, 64)
     e = torch.empty((0, 2, 64), dtype=torch.bfloat16, device=device())
