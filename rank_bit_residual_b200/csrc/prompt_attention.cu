@@ -60,6 +60,7 @@ struct PromptArgs {
   int tile_rows;    // rows of a sequence that an item covers: 128 (two heads) or 256
   int pairs;        // items per row range: heads / 2 or heads
   int shares;       // items that divide an item's keys
+  int group;        // query heads per key head
   float* partial;   // with several shares: [item][share][tile] sums [dim][128], maxima [128], totals [128]
   float scale_log2;
   unsigned* status;
@@ -88,42 +89,50 @@ __device__ __forceinline__ bool bad_cu(const int32_t* cu, int s, long long token
   return cu && (cu[s] < 0 || cu[s + 1] < cu[s] || cu[s + 1] > tokens);
 }
 
-// Sequences that a warp has walked past, and their row ranges.
-struct Walked {
-  int sequences = 0, ranges = 0;
+// 32 sequences of the line, one per lane.
+struct Window {
+  int first = -32;          // sequence of lane 0; below 0: nothing loaded yet
+  int before = 0;           // row ranges of the sequences in front
+  int q0, rows, k0, keys;   // first rows and counts
+  int n, upto;              // row ranges, and those of the lanes up to this one
 };
 
+__device__ __forceinline__ void load_window(const PromptArgs& a, int first, int before, Window& w) {
+  const int lane = threadIdx.x & 31, s = first + lane;
+  w.first = first, w.before = before;
+  w.q0 = w.rows = w.k0 = w.keys = w.n = 0;
+  if (s < a.batch) {
+    w.q0 = static_cast<int>(cu_at(a.cu_q, s, a.q_tokens));
+    w.rows = max(0, static_cast<int>(cu_at(a.cu_q, s + 1, a.q_tokens)) - w.q0);
+    w.k0 = static_cast<int>(cu_at(a.cu_k, s, a.k_tokens));
+    w.keys = max(0, static_cast<int>(cu_at(a.cu_k, s + 1, a.k_tokens)) - w.k0);
+    w.n = (w.rows + a.tile_rows - 1) / a.tile_rows;
+  }
+  w.upto = w.n;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int up = __shfl_up_sync(0xffffffffu, w.upto, o);
+    if (lane >= o) w.upto += up;
+  }
+}
+
 // Item `index` of the line: row ranges of all sequences, each with its `pairs` heads. The
-// whole warp calls it; valid = 0 past the last range. A block's items come in order, so the walk
-// goes on from where the last one ended (from the start each time, 6000 sequences of 7 rows
-// took 42.6 ms instead of 2.9).
-__device__ Item find_item(const PromptArgs& a, int index, Walked& w) {
+// whole warp calls it; valid = 0 past the last range. A block's items come in order, so the
+// window of the last one is kept, and moves on only when it must (from the
+// start each time, 6000 sequences of 7 rows took 42.6 ms instead of 2.8).
+__device__ Item find_item(const PromptArgs& a, int index, Window& w) {
   const int lane = threadIdx.x & 31;
   // every index of the grid passes here, and there are at least as many as sequences
   if (index < a.batch && lane == 0 && (bad_cu(a.cu_q, index, a.q_tokens) || bad_cu(a.cu_k, index, a.k_tokens)))
     record_status(a.status, kStatusEinval);
-  const int whole = index / a.shares, part = index - whole * a.shares;
+  const int whole = a.shares == 1 ? index : index / a.shares, part = index - whole * a.shares;
   const int range = whole / a.pairs, pair = whole - range * a.pairs;
   Item it;
   it.valid = 0;
   it.index = index;
-  if (range < w.ranges) w = Walked();
-  for (; w.sequences < a.batch; w.sequences += 32) {
-    const int before = w.ranges, s = w.sequences + lane;
-    int n = 0, q0 = 0, rows = 0, k0 = 0, keys = 0;
-    if (s < a.batch) {
-      q0 = static_cast<int>(cu_at(a.cu_q, s, a.q_tokens));
-      rows = max(0, static_cast<int>(cu_at(a.cu_q, s + 1, a.q_tokens)) - q0);
-      k0 = static_cast<int>(cu_at(a.cu_k, s, a.k_tokens));
-      keys = max(0, static_cast<int>(cu_at(a.cu_k, s + 1, a.k_tokens)) - k0);
-      n = (rows + a.tile_rows - 1) / a.tile_rows;
-    }
-    int incl = n;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int up = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += up;
-    }
+  if (w.first < 0 || range < w.before) load_window(a, 0, 0, w);
+  while (true) {
+    const int before = w.before, n = w.n, incl = w.upto;
     const unsigned hit = __ballot_sync(0xffffffffu, before + incl > range);
     if (hit != 0) {
       int src = __ffs(hit) - 1;
@@ -147,10 +156,8 @@ __device__ Item find_item(const PromptArgs& a, int index, Walked& w) {
         for (int i = range - skipped; i > 0; --i) has &= has - 1;
         src = __ffs(has) - 1;
       }
-      q0 = __shfl_sync(0xffffffffu, q0, src);
-      rows = __shfl_sync(0xffffffffu, rows, src);
-      k0 = __shfl_sync(0xffffffffu, k0, src);
-      keys = __shfl_sync(0xffffffffu, keys, src);
+      const int q0 = __shfl_sync(0xffffffffu, w.q0, src), rows = __shfl_sync(0xffffffffu, w.rows, src);
+      int k0 = __shfl_sync(0xffffffffu, w.k0, src), keys = __shfl_sync(0xffffffffu, w.keys, src);
       const int r0 = place * a.tile_rows;
       it.valid = 1;
       const bool two_heads = a.tile_rows == kRows;
@@ -179,12 +186,12 @@ __device__ Item find_item(const PromptArgs& a, int index, Walked& w) {
         it.n[t] = it.rows[t] > 0 ? max(0, end + kPart - 1) / kPart : 0;
         it.cut = min(it.cut, max(0, min(keys, it.seen[t])) / kKeys);
       }
-      it.kvh = it.head[0] / (a.q.heads / a.k.heads);
+      it.kvh = it.head[0] / a.group;
       return it;
     }
-    w.ranges += __shfl_sync(0xffffffffu, incl, 31);
+    if (w.first + 32 >= a.batch) return it;
+    load_window(a, w.first + 32, before + __shfl_sync(0xffffffffu, incl, 31), w);
   }
-  return it;
 }
 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
@@ -331,7 +338,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       Turn<Sz::kRing> r;
       uint32_t q_phase = 0, answer_phase = 0, last_raw = 0, raw_phase = 0;   // the last two by ring position
       int index = blockIdx.x;
-      Walked walked;
+      Window window;
       bool ok = true;
       while (ok) {
         // ask for the next item while this one is worked on
@@ -341,7 +348,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         Item it;
         it.valid = 0;
-        if (index >= 0) it = find_item(a, index, walked);
+        if (index >= 0) it = find_item(a, index, window);
         if (index < 0 || it.valid) {
           ok = mbar_wait_warp(&bar.item_empty[slot.i], slot.phase ^ 1, a.status, abort);
           if (ok && lane == 0) {
@@ -778,8 +785,8 @@ template <int kDim>
 __global__ void __launch_bounds__(kJoinThreads) prompt_join_kernel(const __grid_constant__ PromptArgs a) {
   __shared__ Item sh_item;
   if (threadIdx.x < 32) {
-    Walked from_start;
-    const Item it = find_item(a, blockIdx.x * a.shares, from_start);
+    Window window;
+    const Item it = find_item(a, blockIdx.x * a.shares, window);
     if (threadIdx.x == 0) sh_item = it;
   }
   __syncthreads();
@@ -863,7 +870,7 @@ cudaError_t launch_prompt(const svdq_heads& q, const svdq_heads& k, const svdq_h
                           bool* bad_args) {
   const PromptPlan p = plan_prompt(q.heads, k.heads, batch, q_tokens, k_tokens);
   PromptArgs a{q, k, v, out, cu_q, cu_k, batch, q_tokens, k_tokens, head_dim, causal ? 1 : 0,
-               p.tile_rows, p.pairs, p.shares, static_cast<float*>(scratch), scale * 1.4426950408889634f,
+               p.tile_rows, p.pairs, p.shares, q.heads / k.heads, static_cast<float*>(scratch), scale * 1.4426950408889634f,
                device_status_word()};
   CUtensorMap mq, mk, mv;
   // without any key no tile of k or v is ever loaded
