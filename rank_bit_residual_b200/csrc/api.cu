@@ -90,13 +90,14 @@ bool make_tmap_2d(CUtensorMap* map, const void* base, CUtensorMapDataType dtype,
   return r == CUDA_SUCCESS;
 }
 
-bool make_tmap_heads(CUtensorMap* map, const svdq_heads& x, int head_dim, int64_t tokens, uint32_t box_rows) {
+bool make_tmap_heads(CUtensorMap* map, const svdq_heads& x, int head_dim, int64_t tokens, uint32_t box_rows,
+                     uint32_t box_heads) {
   EncodeTiledFn fn = encode_fn();
   if (!fn) return false;
   cuuint64_t dims[3] = {static_cast<cuuint64_t>(head_dim), static_cast<cuuint64_t>(x.heads),
                         static_cast<cuuint64_t>(tokens)};
   cuuint64_t strides[2] = {static_cast<cuuint64_t>(x.head_ld) * 2, static_cast<cuuint64_t>(x.token_ld) * 2};
-  cuuint32_t box[3] = {64, 1, box_rows};
+  cuuint32_t box[3] = {64, box_heads, box_rows};
   cuuint32_t estr[3] = {1, 1, 1};
   return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, x.data, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,

@@ -21,9 +21,10 @@ bool make_tmap_2d(CUtensorMap* map, const void* base, CUtensorMapDataType dtype,
                   int elem_bytes, uint64_t inner, uint64_t outer, uint64_t ld_elems,
                   uint32_t box_inner, uint32_t box_outer, bool swizzle128);
 
-// A map over a bf16 [tokens, heads, head_dim] tensor, loaded in boxes of box_rows tokens
-// of one head by 64 elements with the 128-byte swizzle; zeros outside.
-bool make_tmap_heads(CUtensorMap* map, const svdq_heads& x, int head_dim, int64_t tokens, uint32_t box_rows);
+// A map over a bf16 [tokens, heads, head_dim] tensor, loaded in boxes of box_rows tokens by
+// box_heads heads by 64 elements with the 128-byte swizzle; zeros outside.
+bool make_tmap_heads(CUtensorMap* map, const svdq_heads& x, int head_dim, int64_t tokens, uint32_t box_rows,
+                     uint32_t box_heads = 1);
 
 inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 inline int64_t round_up(int64_t a, int64_t b) { return ceil_div(a, b) * b; }

@@ -3,11 +3,11 @@
 //   out = sum_j p_j v_j / sum_j p_j,   p_j = exp(scale q . k_j - m),   m = the running maximum
 //
 // One pass over the keys with a running maximum and sum. A block works on an item of two
-// tiles of 128 query rows that share their keys: the same rows of two query heads of one
-// key head when the group is even, else 256 consecutive rows of one head. Per tile and 64
-// keys, S = Q K^T goes to tensor memory, four warps (one row per thread, so row maxima
-// and sums need no exchange) turn it into P = 2^(S c - m) in bf16 and put it back over
-// S, and O += P V accumulates in tensor memory with P as the operand from there. Each
+// tiles of 128 rows that share their keys: consecutive rows of a sequence, each with the
+// heads of a key head's group (the largest power of two of them) side by side. Per tile
+// and 64 keys, S = Q K^T goes to tensor memory, four warps (one row per thread, so row
+// maxima and sums need no exchange) turn it into P = 2^(S c - m) in bf16 and put it back
+// over S, and O += P V accumulates in tensor memory with P as the operand from there. Each
 // tile has two S buffers: the products of the next 64 keys run while softmax works on
 // these. (With one buffer of 128 keys, softmax waited for P V and the next S in turn: 3400
 // cycles per 128 keys of both tiles against 2048 of products.)
@@ -47,6 +47,7 @@ constexpr int kRows = 128;      // query rows of a tile
 constexpr int kKeys = 128;      // keys of a loaded tile
 constexpr int kPart = 64;       // keys of a part: what softmax takes at a time
 constexpr int kThreads = 384;
+constexpr int kMaxFold = 5;     // 32 heads in a tile: a warp's rows
 constexpr int kMaxShares = 8;   // items that divide an item's keys
 constexpr int kItems = 4;       // items between the chooser and the slowest reader
 
@@ -57,8 +58,8 @@ struct PromptArgs {
   int batch;
   int64_t q_tokens, k_tokens;
   int dim, causal;
-  int tile_rows;    // rows of a sequence that an item covers: 128 (two heads) or 256
-  int pairs;        // items per row range: heads / 2 or heads
+  int fold;         // log2 of the heads that lie side by side in a tile
+  int pairs;        // items per row range: heads >> fold
   int shares;       // items that divide an item's keys
   int group;        // query heads per key head
   float* partial;   // with several shares: [item][share][tile] sums [dim][128], maxima [128], totals [128]
@@ -73,8 +74,8 @@ struct Item {
   int n[2];         // parts of each row tile
   int cut;          // first loaded tile with a key that some row does not see
   int row[2];       // first row in q and out
-  int rows[2];      // rows inside the sequence, 0 .. 128
-  int head[2];
+  int rows[2];      // rows inside the sequence, 0 .. 128 >> fold
+  int head;         // the first
   int seen[2];      // keys that the tile's first row sees (causal; row r sees r more)
   int index;        // of the item and its share
 };
@@ -106,7 +107,7 @@ __device__ __forceinline__ void load_window(const PromptArgs& a, int first, int 
     w.rows = max(0, static_cast<int>(cu_at(a.cu_q, s + 1, a.q_tokens)) - w.q0);
     w.k0 = static_cast<int>(cu_at(a.cu_k, s, a.k_tokens));
     w.keys = max(0, static_cast<int>(cu_at(a.cu_k, s + 1, a.k_tokens)) - w.k0);
-    w.n = (w.rows + a.tile_rows - 1) / a.tile_rows;
+    w.n = (w.rows + (2 * kRows >> a.fold) - 1) >> (8 - a.fold);   // of 256 >> fold rows
   }
   w.upto = w.n;
 #pragma unroll
@@ -158,16 +159,14 @@ __device__ Item find_item(const PromptArgs& a, int index, Window& w) {
       }
       const int q0 = __shfl_sync(0xffffffffu, w.q0, src), rows = __shfl_sync(0xffffffffu, w.rows, src);
       int k0 = __shfl_sync(0xffffffffu, w.k0, src), keys = __shfl_sync(0xffffffffu, w.keys, src);
-      const int r0 = place * a.tile_rows;
       it.valid = 1;
-      const bool two_heads = a.tile_rows == kRows;
+      it.head = pair << a.fold;
       int last = 0;   // keys that any row sees
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
-        const int row = two_heads ? r0 : r0 + t * kRows;
-        it.head[t] = two_heads ? 2 * pair + t : pair;
+        const int row = (2 * place + t) * (kRows >> a.fold);
         it.row[t] = q0 + row;
-        it.rows[t] = max(0, min(kRows, rows - row));
+        it.rows[t] = max(0, min(kRows >> a.fold, rows - row));
         it.seen[t] = a.causal ? keys - rows + row + 1 : keys;
         if (it.rows[t] > 0) last = max(last, a.causal ? min(keys, it.seen[t] + it.rows[t] - 1) : keys);
       }
@@ -186,7 +185,7 @@ __device__ Item find_item(const PromptArgs& a, int index, Window& w) {
         it.n[t] = it.rows[t] > 0 ? max(0, end + kPart - 1) / kPart : 0;
         it.cut = min(it.cut, max(0, min(keys, it.seen[t])) / kKeys);
       }
-      it.kvh = it.head[0] / a.group;
+      it.kvh = it.head / a.group;
       return it;
     }
     if (w.first + 32 >= a.batch) return it;
@@ -368,7 +367,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int t = 0; t < 2; ++t)
 #pragma unroll
               for (int c = 0; c < kDim / 64; ++c)
-                tma_load_3d(sq + t * Sz::kTile + c * kRows * 128, &map_q, &bar.q_full, c * 64, it.head[t], it.row[t]);
+                tma_load_3d(sq + t * Sz::kTile + c * kRows * 128, &map_q, &bar.q_full, c * 64, it.head, it.row[t]);
           }
           for (int j = 0; ok && j < 2 * n; ++j) {   // K0, V0, K1, V1, ...
             ok = mbar_wait_soon(&bar.empty[r.i], r.phase ^ 1, a.status, abort);
@@ -562,6 +561,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------ softmax and output
     const int t = warp >> 2;
     const int row = (warp & 3) * 32 + lane;   // of the tile
+    const int fold = a.fold, down = row >> fold;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t to = tmem + lanes + Sz::kO + t * kDim;
     // The product takes the sign. A scale of zero is one so small that all weights are 1, and
@@ -577,7 +577,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       const Item& it = items[slot.i];
       if (!it.valid) break;
       const int n = it.n[t];
-      const int seen = a.causal ? min(it.keys, it.seen[t] + row) : it.keys;   // keys of this row
       const int all_see = min(it.keys, it.seen[t]);
       ++number;
       float m = -INFINITY;
@@ -655,7 +654,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_ld_wait_regs(s[1]);
         }
         if (!done) {
-          const int left = seen - j * kPart;
+          const int left = (a.causal ? min(it.keys, it.seen[t] + down) : it.keys) - j * kPart;   // keys of this row
 #pragma unroll
           for (int c = 0; c < 2; ++c)
 #pragma unroll
@@ -694,7 +693,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(&bar.p_full[t][buf]);
       }
       if (!ok) break;
-      const int k0 = it.k0, kvh = it.kvh, cut = it.cut, row0 = it.row[t], rows = it.rows[t], head = it.head[t];
+      const int seen = a.causal ? min(it.keys, it.seen[t] + down) : it.keys;   // keys of this row
+      const int k0 = it.k0, kvh = it.kvh, cut = it.cut, row0 = it.row[t], rows = it.rows[t] << a.fold, head = it.head;
       const int index = it.index;
       __syncwarp();
       if (lane == 0) mbar_arrive(&bar.item_empty[slot.i]);
@@ -719,8 +719,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         partial[(kDim + 1) * kRows] = l;
       }
       const bool extra = n > 0 && odd[number % (2 * kItems)] == number;
-      __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.out.data) +   // of the warp's first row
-                           static_cast<long long>(row0 + (warp & 3) * 32) * a.out.token_ld + head * a.out.head_ld;
+      __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.out.data) + row0 * a.out.token_ld + head * a.out.head_ld;
       unsigned char* stage = ring + Sz::kRing * Sz::kTile + warp * 4096;
 #pragma unroll
       for (int c = 0; c < kDim / 32; ++c) {
@@ -761,10 +760,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int col = (c - 1) * 32 + (lane & 7) * 8;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const int r = i * 4 + (lane >> 3);
+          const int r = i * 4 + (lane >> 3), at = (warp & 3) * 32 + r;   // of the warp, of the tile
           const uint4 v = *reinterpret_cast<const uint4*>(stage + r * 128 + (((lane & 7) ^ (r & 7)) << 4));
-          if ((warp & 3) * 32 + r < rows && col < a.dim)
-            *reinterpret_cast<uint4*>(dst + r * a.out.token_ld + col) = v;
+          if (at < rows && col < a.dim)
+            *reinterpret_cast<uint4*>(dst + ((at >> fold) * a.out.token_ld + (at & ((1 << fold) - 1)) * a.out.head_ld) +
+                                      col) = v;
         }
       }
       tc_fence_before();
@@ -792,7 +792,7 @@ __global__ void __launch_bounds__(kJoinThreads) prompt_join_kernel(const __grid_
   __syncthreads();
   pdl_wait();
   const int t = blockIdx.y, row = threadIdx.x % kRows, eighth = blockIdx.z * 2 + threadIdx.x / kRows;
-  if (!sh_item.valid || row >= sh_item.rows[t]) return;
+  if (!sh_item.valid || row >= sh_item.rows[t] << a.fold) return;
   const int step = 2 * partial_floats<kDim>();   // from share to share
   const float* p = a.partial + (static_cast<long long>(blockIdx.x) * a.shares * 2 + t) * partial_floats<kDim>() + row;
   float top = -INFINITY;
@@ -806,7 +806,8 @@ __global__ void __launch_bounds__(kJoinThreads) prompt_join_kernel(const __grid_
   }
   const float inv = total == 0.0f ? 0.0f : 1.0f / total;
   __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.out.data) +
-                       static_cast<long long>(sh_item.row[t] + row) * a.out.token_ld + sh_item.head[t] * a.out.head_ld;
+                       (sh_item.row[t] + (row >> a.fold)) * a.out.token_ld +
+                       (sh_item.head + (row & ((1 << a.fold) - 1))) * a.out.head_ld;
   for (int d = eighth * (kDim / 8); d < (eighth + 1) * (kDim / 8) && d < a.dim; d += 8) {
     float x[8] = {};
 #pragma unroll
@@ -823,18 +824,20 @@ __global__ void __launch_bounds__(kJoinThreads) prompt_join_kernel(const __grid_
 
 // How an item is made up, and how many there are at most.
 struct PromptPlan {
-  int tile_rows, pairs, shares;
+  int fold, pairs, shares;
   int64_t items;
 };
 
 PromptPlan plan_prompt(int heads, int kv_heads, int batch, int64_t q_tokens, int64_t k_tokens) {
   PromptPlan p;
-  // Two heads that share their keys make a better pair than two row ranges: both tiles see
-  // the same keys, and a sequence's last range wastes fewer rows.
-  const bool two_heads = heads / kv_heads % 2 == 0;
-  p.tile_rows = two_heads ? kRows : 2 * kRows;
-  p.pairs = two_heads ? heads / 2 : heads;
-  p.items = (q_tokens / p.tile_rows + batch) * p.pairs;
+  // Heads that share their keys lie side by side in a tile, a power of two of them: fewer rows
+  // of the sequence then are in it, of which fewer lie behind its end or beside the diagonal
+  // (with two side by side 9 ragged prompts of 32 on 8 heads took 98.7 us instead of 96.5, 1000 sequences
+  // of 30 rows 525 instead of 278).
+  const int group = heads / kv_heads;
+  for (p.fold = 0; p.fold < kMaxFold && group % (2 << p.fold) == 0;) ++p.fold;
+  p.pairs = heads >> p.fold;
+  p.items = (q_tokens / (2 * kRows >> p.fold) + batch) * p.pairs;
   // As many shares as fill the SMs once, each of a thousand keys or more on average: below
   // that the join takes what the shares gain.
   const int64_t fill = num_sms() / std::max<int64_t>(p.items, 1), keys = k_tokens / std::max(batch, 1) / 1024;
@@ -870,11 +873,11 @@ cudaError_t launch_prompt(const svdq_heads& q, const svdq_heads& k, const svdq_h
                           bool* bad_args) {
   const PromptPlan p = plan_prompt(q.heads, k.heads, batch, q_tokens, k_tokens);
   PromptArgs a{q, k, v, out, cu_q, cu_k, batch, q_tokens, k_tokens, head_dim, causal ? 1 : 0,
-               p.tile_rows, p.pairs, p.shares, q.heads / k.heads, static_cast<float*>(scratch), scale * 1.4426950408889634f,
+               p.fold, p.pairs, p.shares, q.heads / k.heads, static_cast<float*>(scratch), scale * 1.4426950408889634f,
                device_status_word()};
   CUtensorMap mq, mk, mv;
   // without any key no tile of k or v is ever loaded
-  *bad_args = !make_tmap_heads(&mq, q, head_dim, q_tokens, kRows) ||
+  *bad_args = !make_tmap_heads(&mq, q, head_dim, q_tokens, kRows >> p.fold, 1u << p.fold) ||
               !make_tmap_heads(&mk, k_tokens > 0 ? k : q, head_dim, k_tokens > 0 ? k_tokens : q_tokens, kKeys) ||
               !make_tmap_heads(&mv, k_tokens > 0 ? v : q, head_dim, k_tokens > 0 ? k_tokens : q_tokens, kKeys);
   if (*bad_args) return cudaSuccess;

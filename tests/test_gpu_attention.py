@@ -68,6 +68,47 @@ def test_prompt_head_groups(H, K):
     run_prompt([200], [333], H, K, 128, True, seed=H)
 
 
+@pytest.mark.parametrize("H,K", [(4, 1), (6, 1), (16, 2), (16, 1), (32, 1), (64, 1), (48, 2)])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("causal", [True, False])
+def test_prompt_heads_side_by_side(H, K, D, causal):
+    """Groups of every power of two (and with another factor), sequences that end inside a tile."""
+    run_prompt([1, 31, 33, 0, 70, 9], [1, 40, 33, 5, 66, 130], H, K, D, causal, seed=H + K + D)
+
+
+@pytest.mark.parametrize("H,K", [(4, 1), (32, 1)])
+def test_prompt_heads_side_by_side_few_rows_many_keys(H, K):
+    run_prompt([9, 3], [5000, 4100], H, K, 128, True, seed=H)
+    run_prompt([70], [6000], H, K, 64, False, seed=H)
+
+
+@pytest.mark.parametrize("H", [4, 8])
+def test_prompt_heads_side_by_side_in_heads_major_tensors(H):
+    """Strides of heads larger than those of tokens; rows around the sequences stay."""
+    T, D = 90, 64
+    q = draw(1, H, T, D).transpose(0, 1)
+    k, v = draw(2, T, 1, D), draw(3, T, 1, D)
+    out = torch.full((H, T, D), 7.0, dtype=torch.bfloat16, device=device()).transpose(0, 1)
+    cu = [5, 20, 20, 77]
+    rb.svdq_attention_prompt(q, k, v, ints(cu), ints(cu), out=out)
+    want, spread, reach = oa.prompt(f64(q), f64(k), f64(v), cu, cu, 0.125, True)
+    close(out[5:77], want[5:77], spread[5:77], reach, D, 57, "heads major")
+    assert torch.all(out[:5] == 7) and torch.all(out[77:] == 7)
+
+
+def test_prompt_heads_side_by_side_values_without_end():
+    """A row and all its heads see the infinity at their own key and no later one."""
+    T, H, D = 50, 8, 128
+    q, k, v = draw(1, T, H, D), draw(2, T, 1, D), draw(3, T, 1, D)
+    clean = rb.svdq_attention_prompt(q, k, v)
+    v[20, 0, 3] = float("inf")
+    v[30, 0, 5] = float("nan")
+    got = rb.svdq_attention_prompt(q, k, v)
+    assert torch.equal(got[:20], clean[:20])
+    assert torch.isinf(got[20:30, :, 3]).all() and torch.isfinite(got[20:30, :, 4:]).all()
+    assert torch.isnan(got[30:, :, 5]).all() and torch.isinf(got[30:, :, 3]).all()
+
+
 def test_prompt_large_scores_and_scales():
     run_prompt([300], [300], 2, 2, 128, True, q_gain=8.0)          # scores up to hundreds: one key wins
     run_prompt([300], [300], 2, 2, 64, False, scale=0.0)           # the plain mean
