@@ -561,7 +561,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------ softmax and output
     const int t = warp >> 2;
     const int row = (warp & 3) * 32 + lane;   // of the tile
-    const int fold = a.fold, down = row >> fold;
+    const int down = row >> a.fold;           // of the sequence, from the tile's first
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t to = tmem + lanes + Sz::kO + t * kDim;
     // The product takes the sign. A scale of zero is one so small that all weights are 1, and
@@ -720,23 +720,48 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       const bool extra = n > 0 && odd[number % (2 * kItems)] == number;
       __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.out.data) + row0 * a.out.token_ld + head * a.out.head_ld;
-      unsigned char* stage = ring + Sz::kRing * Sz::kTile + warp * 4096;
+      if (extra) {   // hardly ever, so short rather than fast: the values taken out are added
+        const __nv_bfloat16* vp = static_cast<const __nv_bfloat16*>(a.v.data) + kvh * a.v.head_ld;
+        dst += down * a.out.token_ld + (row & ((1 << a.fold) - 1)) * a.out.head_ld;
+#pragma unroll 1
+        for (int c = 0; c < a.dim; c += 16) {
+          uint32_t o[16];
+          __syncwarp();
+          tmem_ld_32x32b_x16(to + c, o);
+          tmem_ld_wait_regs(o);
+          if (row >= rows) continue;
+          for (int key = cut * kKeys; key < seen; ++key)
 #pragma unroll
-      for (int c = 0; c < kDim / 32; ++c) {
+            for (int i = 0; i < 16; ++i) {
+              const float x = c + i < a.dim ? __bfloat162float(vp[(k0 + key) * a.v.token_ld + c + i]) : 0.0f;
+              if (!isfinite(x)) o[i] = __float_as_uint(__uint_as_float(o[i]) + x);
+            }
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            if (c + i >= a.dim) continue;
+            if (kShared)
+              partial[(c + i) * kRows] = __uint_as_float(o[i]);
+            else
+              dst[c + i] = __float2bfloat16_rn(__uint_as_float(o[i]) * inv);
+          }
+        }
+        __syncwarp();
+        tc_fence_before();
+        continue;
+      }
+      unsigned char* stage = ring + Sz::kRing * Sz::kTile + warp * 4096;
+      // Short code: a block runs through it once per item, so it waits for instructions (unrolled,
+      // and with the rare case above in it, 1000 sequences of 30 rows took 277 us instead of 242).
+#pragma unroll 1
+      for (int pair = 0; pair < kDim / 64; ++pair)
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        const int c = 2 * pair + half;
         uint32_t o[32];
         __syncwarp();
         if (n > 0) {
           tmem_ld_32x32b_x32(to + c * 32, o);
           tmem_ld_wait_regs(o);
-        }
-        if (extra && row < rows) {
-          const __nv_bfloat16* vp = static_cast<const __nv_bfloat16*>(a.v.data) + kvh * a.v.head_ld;
-          for (int key = cut * kKeys; key < seen; ++key)
-#pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              const float x = c * 32 + i < a.dim ? __bfloat162float(vp[(k0 + key) * a.v.token_ld + c * 32 + i]) : 0.0f;
-              if (!isfinite(x)) o[i] = __float_as_uint(__uint_as_float(o[i]) + x);
-            }
         }
         if (kShared) {
 #pragma unroll
@@ -763,7 +788,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int r = i * 4 + (lane >> 3), at = (warp & 3) * 32 + r;   // of the warp, of the tile
           const uint4 v = *reinterpret_cast<const uint4*>(stage + r * 128 + (((lane & 7) ^ (r & 7)) << 4));
           if (at < rows && col < a.dim)
-            *reinterpret_cast<uint4*>(dst + ((at >> fold) * a.out.token_ld + (at & ((1 << fold) - 1)) * a.out.head_ld) +
+            *reinterpret_cast<uint4*>(dst + ((at >> a.fold) * a.out.token_ld + (at & ((1 << a.fold) - 1)) * a.out.head_ld) +
                                       col) = v;
         }
       }
@@ -833,7 +858,7 @@ PromptPlan plan_prompt(int heads, int kv_heads, int batch, int64_t q_tokens, int
   // Heads that share their keys lie side by side in a tile, a power of two of them: fewer rows
   // of the sequence then are in it, of which fewer lie behind its end or beside the diagonal
   // (with two side by side 9 ragged prompts of 32 on 8 heads took 98.7 us instead of 96.5, 1000 sequences
-  // of 30 rows 525 instead of 278).
+  // of 30 rows 525 instead of 278 at the time).
   const int group = heads / kv_heads;
   for (p.fold = 0; p.fold < kMaxFold && group % (2 << p.fold) == 0;) ++p.fold;
   p.pairs = heads >> p.fold;

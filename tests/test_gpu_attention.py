@@ -109,6 +109,20 @@ def test_prompt_heads_side_by_side_values_without_end():
     assert torch.isnan(got[30:, :, 5]).all() and torch.isinf(got[30:, :, 3]).all()
 
 
+@pytest.mark.parametrize("D", [8, 24, 64, 72, 120])
+@pytest.mark.parametrize("T,K,H", [(150, 150, 2), (40, 9000, 4), (300, 300, 1)])
+def test_prompt_values_without_end(T, K, H, D):
+    """One infinity in V: its column is infinite for the rows that see it, all else is as without it."""
+    q, k, v = draw(1, T, H, D), draw(2, K, 1, D), draw(3, K, 1, D)
+    clean = rb.svdq_attention_prompt(q, k, v)
+    first, col = T - 30, D - 3               # the first row that sees it
+    v[K - T + first, 0, col] = float("-inf")
+    got = rb.svdq_attention_prompt(q, k, v)
+    assert torch.all(got[first:, :, col] == float("-inf"))
+    got[first:, :, col] = clean[first:, :, col]
+    assert torch.equal(got, clean)
+
+
 def test_prompt_large_scores_and_scales():
     run_prompt([300], [300], 2, 2, 128, True, q_gain=8.0)          # scores up to hundreds: one key wins
     run_prompt([300], [300], 2, 2, 64, False, scale=0.0)           # the plain mean
