@@ -639,9 +639,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           const bool there = j + 1 < n && mbar_test(&bar.s_full[t][buf ^ 1], (s_phase >> (buf ^ 1)) & 1);
           largest(1, tops);
           weights(1, std::integral_constant<int, Sz::kPoly>{}, scale2, base2, add);
-          // (a row that has seen nothing but -inf, m = -inf, is not done either)
           const float top = max3_nan(tops[0], tops[1], tops[1]) * scale;
-          done = __all_sync(0xffffffffu, top <= m + 8.0f && m > -INFINITY);
+          // Not where a row has seen nothing but -inf (m = -inf). Both forms say so; the compiler finds
+          // better registers with the first for heads of 128 elements (512 sequences of 128 rows:
+          // 286 us, with the second 310) and with the second for 64 (2 x 2048 rows: 117.5 us, with
+          // the first 121).
+          const bool small = kDim == 128 ? top <= m + 8.0f && m > -INFINITY : top - m <= 8.0f;
+          // Rows behind the sequence's end hold whatever lies there and are never stored: they
+          // decide nothing for the rows beside them in the warp.
+          done = __all_sync(0xffffffffu, small || row >= it.rows[t] << a.fold);
           if (done) {
             sums[0] = add[0], sums[1] = add[1];
             ahead = __all_sync(0xffffffffu, there);
