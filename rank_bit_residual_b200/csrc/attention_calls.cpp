@@ -145,6 +145,10 @@ bool number(PyObject* o, float* x) {
   return true;
 }
 
+// 1 / sqrt(head_dim), rounded once, as the long way has it (in fp32 throughout it is a step off for
+// heads of 24, 72, 96 and 112).
+float default_scale(int64_t dim) { return static_cast<float>(1.0 / std::sqrt(static_cast<double>(dim))); }
+
 svdq_kv_cache cache(Call& c, const at::Tensor* k, const at::Tensor* v) {
   svdq_kv_cache r{};
   int64_t ks[3], vs[3];
@@ -272,7 +276,7 @@ PyObject* prompt(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const void* cq = c.vector(cu_q, at::kInt, batch + 1);
     const void* ck = c.vector(cu_k, at::kInt, batch + 1);
     const int causal = PyObject_IsTrue(a[5]);
-    float scale = 1.0f / std::sqrt(static_cast<float>(dim));
+    float scale = default_scale(dim);
     if (!c.good || causal < 0 || batch < 1 || batch > INT32_MAX || dim > INT32_MAX || kh.heads != vh.heads ||
         (a[6] != Py_None && !number(a[6], &scale)))
       return nullptr;
@@ -304,7 +308,7 @@ PyObject* decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (!c.good) return nullptr;
     const int64_t batch = q->size(0);
     const void* len = c.vector(lens, at::kInt, batch);
-    float scale = 1.0f / std::sqrt(static_cast<float>(store.head_dim));
+    float scale = default_scale(store.head_dim);
     if (!c.good || batch > INT32_MAX || table->scalar_type() != at::kInt || table->dim() != 2 || table->size(0) != batch ||
         !table->is_contiguous() || (a[5] != Py_None && !number(a[5], &scale)))
       return nullptr;
