@@ -29,8 +29,11 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import importlib.util
 import math
+import os
 from dataclasses import dataclass
+from importlib.machinery import ExtensionFileLoader
 from typing import Optional, Tuple
 
 import torch
@@ -86,7 +89,7 @@ _NO_HEADS = SvdqHeads(None, 0, 0, 0)
 _NO_ROPE = SvdqRope(None, 0, 0, 1.0)
 
 # A decode step calls these functions between kernels of a few microseconds, so their host
-# work counts. The usual call goes through _calls.so (csrc/attention_calls.cpp), which reads
+# work counts. The usual call goes through _calls.*.so (csrc/attention_calls.cpp), which reads
 # the tensors directly: 5 us. What it does not take - a copy to make, another device than the
 # current one, a mistake to name - comes back as None and goes the long way below: 15 us.
 
@@ -94,15 +97,24 @@ _calls = None
 _calls_lib = None
 
 
+def _load_calls():
+    """The module built for this Python and this torch, and no other."""
+    from . import build
+    path = build.calls_path()
+    if not os.path.exists(path):
+        raise ImportError(f"{path} not built; run python -m rank_bit_residual_b200.build")
+    loader = ExtensionFileLoader("rank_bit_residual_b200._calls", path)
+    module = importlib.util.module_from_spec(importlib.util.spec_from_file_location(loader.name, path, loader=loader))
+    loader.exec_module(module)
+    return module
+
+
 def _quick():
     """The module of quick calls, bound to the loaded library."""
     global _calls, _calls_lib
     lib = load_library()
     if _calls_lib is not lib:
-        try:
-            from . import _calls as module
-        except ImportError as e:
-            raise ImportError("_calls.so not built; run python -m rank_bit_residual_b200.build") from e
+        module = _load_calls()
         module.bind(*(ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in (
             "svdq_qk_norm_rope", "svdq_kv_append", "svdq_attention_prompt", "svdq_attention_prompt_workspace_size",
             "svdq_attention_decode", "svdq_attention_decode_workspace_size")))

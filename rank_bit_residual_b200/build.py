@@ -7,7 +7,8 @@ objects are linked into rank_bit_residual_b200/libsvdq.so. The CUDA runtime is
 linked statically; the driver API is reached through cudaGetDriverEntryPoint,
 so loading the library needs no libcuda at link time. csrc/attention_calls.cpp, the
 quick calls of the attention operators, is compiled against torch and Python with the host
-compiler and becomes rank_bit_residual_b200/_calls.so.
+compiler and becomes rank_bit_residual_b200/_calls.<Python's ABI>.torch-<version>.so: it reads torch's
+own types, so another Python or torch looks for another file and never takes this one.
 """
 
 from __future__ import annotations
@@ -25,7 +26,6 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libsvdq.so")
 CALLS_SRC = os.path.join(CSRC, "attention_calls.cpp")
-CALLS = os.path.join(PKG, "_calls.so")
 INCLUDE = os.path.join(ROOT, "include")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
@@ -56,9 +56,19 @@ def up_to_date() -> bool:
     return all(os.path.getmtime(d) <= t for d in _deps())
 
 
+def calls_path() -> str:
+    """Where the quick calls for this Python and this torch are."""
+    import torch
+    abi = f"{sysconfig.get_config_var('SOABI')}.torch-{torch.__version__}"
+    if not torch.compiled_with_cxx11_abi():
+        abi += "-oldabi"
+    return os.path.join(PKG, f"_calls.{abi}.so")
+
+
 def calls_up_to_date() -> bool:
+    path = calls_path()
     deps = [CALLS_SRC] + glob.glob(os.path.join(INCLUDE, "*.h"))
-    return os.path.exists(CALLS) and all(os.path.getmtime(d) <= os.path.getmtime(CALLS) for d in deps)
+    return os.path.exists(path) and all(os.path.getmtime(d) <= os.path.getmtime(path) for d in deps)
 
 
 def calls_command(out: str):
@@ -80,7 +90,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
     procs = []
     calls = None
     if force or not calls_up_to_date():
-        calls = CALLS + ".tmp"
+        calls = calls_path() + ".tmp"
         procs.append((CALLS_SRC, subprocess.Popen(calls_command(calls), stdout=subprocess.PIPE,
                                                   stderr=subprocess.STDOUT)))
     build_lib = force or not up_to_date()
@@ -105,7 +115,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
         msg = "\n".join(f"--- {s}\n{o}" for s, o in failed)
         raise RuntimeError(f"the compiler failed:\n{msg}")
     if calls:
-        os.replace(calls, CALLS)
+        os.replace(calls, calls_path())
     if not build_lib:
         return LIB
     tmp = LIB + ".tmp"

@@ -1,0 +1,32 @@
+"""What build() makes and when: the library, and the quick calls of the attention operators,
+which belong to one Python and one torch."""
+
+import os
+import sysconfig
+
+import pytest
+import torch
+
+import rank_bit_residual_b200.attention as rba
+from rank_bit_residual_b200 import build as rbuild
+
+
+def test_quick_calls_are_built_and_loaded():
+    rbuild.build()
+    assert rbuild.calls_up_to_date()
+    assert hasattr(rba._load_calls(), "prompt")
+
+
+def test_quick_calls_of_another_torch_or_python_are_not_taken(monkeypatch):
+    rbuild.build()
+    here = rbuild.calls_path()
+    assert torch.__version__ in here and sysconfig.get_config_var("SOABI") in here
+    for change in (lambda m: m.setattr(torch, "__version__", "9.9.9"),
+                   lambda m: m.setattr(sysconfig, "get_config_var", lambda name: "cpython-399-x86_64-linux-gnu"),
+                   lambda m: m.setattr(torch, "compiled_with_cxx11_abi", lambda: False)):
+        with monkeypatch.context() as m:
+            change(m)
+            assert rbuild.calls_path() != here and not rbuild.calls_up_to_date()
+            with pytest.raises(ImportError, match="not built"):
+                rba._load_calls()
+    assert rbuild.calls_up_to_date() and os.path.exists(here)
