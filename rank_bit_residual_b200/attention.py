@@ -32,6 +32,7 @@ import functools
 import importlib.util
 import math
 import os
+import warnings
 from dataclasses import dataclass
 from importlib.machinery import ExtensionFileLoader
 from typing import Optional, Tuple
@@ -110,14 +111,20 @@ def _load_calls():
 
 
 def _quick():
-    """The module of quick calls, bound to the loaded library."""
+    """The module of quick calls, bound to the loaded library; None, after one warning, where it
+    is not there (built without torch's headers, say): all goes the long way then."""
     global _calls, _calls_lib
     lib = load_library()
     if _calls_lib is not lib:
-        module = _load_calls()
-        module.bind(*(ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in (
-            "svdq_qk_norm_rope", "svdq_kv_append", "svdq_attention_prompt", "svdq_attention_prompt_workspace_size",
-            "svdq_attention_decode", "svdq_attention_decode_workspace_size")))
+        try:
+            module = _load_calls()
+            module.bind(*(ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in (
+                "svdq_qk_norm_rope", "svdq_kv_append", "svdq_attention_prompt", "svdq_attention_prompt_workspace_size",
+                "svdq_attention_decode", "svdq_attention_decode_workspace_size")))
+        except ImportError as e:
+            warnings.warn(f"attention calls without the quick way, some 10 us of host work slower: {e}", RuntimeWarning,
+                          stacklevel=3)
+            module = None
         _calls, _calls_lib = module, lib
     return _calls
 
@@ -281,9 +288,11 @@ def svdq_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, positions: Optional[torc
     fp32. q_out=q, k_out=k work in place. Returns (q_out, k_out).
     """
     turns, inter, amp = (None, False, 1.0) if rope is None else (rope.turns, rope.interleaved, rope.amplitude)
-    done = _quick().norm_rope(q, k, positions, turns, inter, amp, q_weight, k_weight, eps, q_out, k_out)
-    if done is not None:
-        return done
+    quick = _quick()
+    if quick is not None:
+        done = quick.norm_rope(q, k, positions, turns, inter, amp, q_weight, k_weight, eps, q_out, k_out)
+        if done is not None:
+            return done
     return _qk_norm_rope(q, k, positions, rope, q_weight, k_weight, eps, q_out, k_out)
 
 
@@ -326,10 +335,11 @@ def svdq_kv_append(k_cache: torch.Tensor, v_cache: torch.Tensor, k: torch.Tensor
     twice. q [T, H, D] is normed and rotated in the same pass. k_out receives the
     finished keys too (k_out=k: in place). Returns q_out (None without q).
     """
-    if q is not None:
+    quick = _quick() if q is not None else None
+    if quick is not None:
         turns, inter, amp = (None, False, 1.0) if rope is None else (rope.turns, rope.interleaved, rope.amplitude)
-        done = _quick().append(k_cache, v_cache, k, v, slots, positions, turns, inter, amp, k_weight, eps, q, q_weight,
-                               q_out, k_out)
+        done = quick.append(k_cache, v_cache, k, v, slots, positions, turns, inter, amp, k_weight, eps, q, q_weight,
+                            q_out, k_out)
         if done is not None:
             return done
     return _kv_append(k_cache, v_cache, k, v, slots, positions, rope, k_weight, eps, q, q_weight, q_out, k_out)
@@ -393,8 +403,9 @@ def svdq_attention_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_
     Scratch (few rows over many keys need some) is allocated per call unless a workspace
     is given (one per stream in flight). Returns [Tq, H, D].
     """
-    if workspace is None:
-        done = _quick().prompt(q, k, v, cu_q, cu_k, causal, scale, out)
+    quick = _quick() if workspace is None else None
+    if quick is not None:
+        done = quick.prompt(q, k, v, cu_q, cu_k, causal, scale, out)
         if done is not None:
             return done
     return _attention_prompt(q, k, v, cu_q, cu_k, causal, scale, out, workspace)
@@ -456,8 +467,9 @@ def svdq_attention_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch
     [B] (0: a zero row). The scratch is allocated per call unless a workspace is given
     (one per stream in flight). Returns [B, H, D].
     """
-    if workspace is None:
-        done = _quick().decode(q, k_cache, v_cache, page_table, kv_len, scale, out)
+    quick = _quick() if workspace is None else None
+    if quick is not None:
+        done = quick.decode(q, k_cache, v_cache, page_table, kv_len, scale, out)
         if done is not None:
             return done
     return _attention_decode(q, k_cache, v_cache, page_table, kv_len, scale, out, workspace)

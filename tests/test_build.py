@@ -3,6 +3,7 @@ which belong to one Python and one torch."""
 
 import os
 import sysconfig
+import warnings
 
 import pytest
 import torch
@@ -30,3 +31,17 @@ def test_quick_calls_of_another_torch_or_python_are_not_taken(monkeypatch):
             with pytest.raises(ImportError, match="not built"):
                 rba._load_calls()
     assert rbuild.calls_up_to_date() and os.path.exists(here)
+
+
+def test_without_quick_calls_the_long_way_is_taken(monkeypatch, tmp_path):
+    """One warning, and the calls go on to the checks of the long way."""
+    monkeypatch.setattr(rbuild, "calls_path", lambda: str(tmp_path / "none.so"))
+    monkeypatch.setattr(rba, "_calls_lib", None)
+    monkeypatch.setattr(rba, "_calls", None)
+    t = torch.zeros((2, 4, 64), dtype=torch.bfloat16)
+    with pytest.warns(RuntimeWarning, match="quick way"), pytest.raises(ValueError):
+        rba.svdq_qk_norm_rope(t, t)                                  # host tensors
+    with warnings.catch_warnings():
+        warnings.simplefilter("error")
+        with pytest.raises(ValueError):
+            rba.svdq_attention_prompt(t, t, t)

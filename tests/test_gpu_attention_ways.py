@@ -9,6 +9,7 @@ import torch
 
 import rank_bit_residual_b200 as rb
 import rank_bit_residual_b200.attention as rba
+from rank_bit_residual_b200 import build as rbuild
 from tests.gpu_util import device
 
 pytestmark = pytest.mark.gpu
@@ -78,4 +79,31 @@ def test_a_workspace_or_a_copy_changes_no_bit(D):
     assert torch.equal(rb.svdq_attention_decode(dq, kc, vc, table, lens, workspace=rb.LinearWorkspace()), quick)
     assert torch.equal(rb.svdq_attention_decode(shifted, kc, vc, table, lens), quick)
     assert torch.equal(rb.svdq_attention_decode(dq, kc, vc, table, lens, scale=1.0 / math.sqrt(D)), quick)
+    assert rb.svdq_check_status() == rb.SVDQ_OK
+
+
+def test_all_calls_without_the_quick_calls(monkeypatch, tmp_path):
+    """The library alone is enough: the same bits, after a warning."""
+    T, H, K, D = 40, 4, 2, 64
+    row = draw(1, T, (H + 2 * K) * D)
+    q, k, v = row.view(T, -1, D).split([H, K, K], 1)
+    w, pos, rope = draw(2, D), torch.arange(T, device=device()), rb.Rope.make(D)
+
+    def all_four():
+        kc, vc = (torch.zeros((4, 16, K, D), dtype=torch.bfloat16, device=device()) for _ in range(2))
+        a, b = rb.svdq_qk_norm_rope(q, k, pos, rope, w, w)
+        c = rb.svdq_kv_append(kc, vc, k, v, pos, pos, rope, w, q=q, q_weight=w)
+        o = rb.svdq_attention_prompt(a, b, v)
+        d = rb.svdq_attention_decode(a[-1:], kc, vc, ints([[0, 1, 2]]), ints([T]))
+        return a, b, c, kc, vc, o, d
+
+    want = all_four()
+    monkeypatch.setattr(rbuild, "calls_path", lambda: str(tmp_path / "none.so"))
+    monkeypatch.setattr(rba, "_calls_lib", None)
+    monkeypatch.setattr(rba, "_calls", None)
+    with pytest.warns(RuntimeWarning, match="quick way"):
+        got = all_four()
+    assert rba._quick() is None
+    for x, y in zip(got, want):
+        assert torch.equal(x, y)
     assert rb.svdq_check_status() == rb.SVDQ_OK
