@@ -94,6 +94,8 @@ def build(force: bool = False, verbose: bool = False) -> str:
         procs.append((CALLS_SRC, subprocess.Popen(calls_command(calls), stdout=subprocess.PIPE,
                                                   stderr=subprocess.STDOUT)))
     build_lib = force or not up_to_date()
+    if not build_lib and not procs:
+        return LIB
     os.makedirs(BUILD, exist_ok=True)
     cc = nvcc()
     objs = []

@@ -45,3 +45,13 @@ def test_without_quick_calls_the_long_way_is_taken(monkeypatch, tmp_path):
         warnings.simplefilter("error")
         with pytest.raises(ValueError):
             rba.svdq_attention_prompt(t, t, t)
+
+
+def test_nothing_to_build_needs_no_compiler(monkeypatch):
+    """Where library and quick calls are up to date, build() asks for no toolkit."""
+    rbuild.build()
+
+    def none():
+        raise RuntimeError("no nvcc here")
+    monkeypatch.setattr(rbuild, "nvcc", none)
+    assert rbuild.build() == rbuild.LIB
