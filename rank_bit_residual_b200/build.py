@@ -19,6 +19,7 @@ import shutil
 import subprocess
 import sys
 import sysconfig
+import warnings
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -85,21 +86,47 @@ def calls_command(out: str):
             "-L" + lib, "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
 
 
+def _start_calls(force: bool):
+    """The compiler of the quick calls at work, why it cannot be, or None: nothing to do."""
+    try:
+        if not force and calls_up_to_date():
+            return None
+        return subprocess.Popen(calls_command(calls_path() + ".tmp"), stdout=subprocess.PIPE, stderr=subprocess.STDOUT)
+    except (ImportError, OSError, RuntimeError) as e:   # no torch, no g++, no CUDA headers
+        return str(e)
+
+
+def _finish_calls(calls) -> None:
+    """The library is complete without the quick calls, so a failure is a warning."""
+    if not isinstance(calls, str):
+        out, _ = calls.communicate()
+        if calls.returncode == 0:
+            os.replace(calls_path() + ".tmp", calls_path())
+            return
+        calls = out.decode(errors="replace")
+    warnings.warn(f"the quick calls of the attention operators were not built, the calls without them are:\n{calls}",
+                  RuntimeWarning, stacklevel=3)
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile and link; returns the library path. Raises on any compiler error."""
-    procs = []
-    calls = None
-    if force or not calls_up_to_date():
-        calls = calls_path() + ".tmp"
-        procs.append((CALLS_SRC, subprocess.Popen(calls_command(calls), stdout=subprocess.PIPE,
-                                                  stderr=subprocess.STDOUT)))
-    build_lib = force or not up_to_date()
-    if not build_lib and not procs:
-        return LIB
+    """Compile and link; returns the library path. Raises if the library cannot be built, and
+    warns if only the quick calls cannot."""
+    calls = _start_calls(force)
+    try:
+        if force or not up_to_date():
+            _build_library(verbose)
+    finally:
+        if calls is not None:
+            _finish_calls(calls)
+    return LIB
+
+
+def _build_library(verbose: bool) -> None:
     os.makedirs(BUILD, exist_ok=True)
     cc = nvcc()
+    procs = []
     objs = []
-    for src in sources() if build_lib else ():
+    for src in sources():
         obj = os.path.join(BUILD, os.path.basename(src)[:-3] + ".o")
         objs.append(obj)
         cmd = [cc, *ARCH, *FLAGS, "-c", src, "-o", obj]
@@ -115,18 +142,13 @@ def build(force: bool = False, verbose: bool = False) -> str:
             print(out.decode(errors="replace"))
     if failed:
         msg = "\n".join(f"--- {s}\n{o}" for s, o in failed)
-        raise RuntimeError(f"the compiler failed:\n{msg}")
-    if calls:
-        os.replace(calls, calls_path())
-    if not build_lib:
-        return LIB
+        raise RuntimeError(f"nvcc failed:\n{msg}")
     tmp = LIB + ".tmp"
     cmd = [cc, *ARCH, "-shared", "-Xcompiler", "-fPIC", "-o", tmp, *objs]
     r = subprocess.run(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)
     if r.returncode != 0:
         raise RuntimeError("link failed:\n" + r.stdout.decode(errors="replace"))
     os.replace(tmp, LIB)
-    return LIB
 
 
 if __name__ == "__main__":

@@ -55,3 +55,47 @@ def test_nothing_to_build_needs_no_compiler(monkeypatch):
         raise RuntimeError("no nvcc here")
     monkeypatch.setattr(rbuild, "nvcc", none)
     assert rbuild.build() == rbuild.LIB
+
+
+@pytest.fixture
+def small_tree(monkeypatch, tmp_path):
+    """A tree of one source with a stand-in for nvcc, which makes the file that -o names."""
+    src = tmp_path / "csrc"
+    src.mkdir()
+    (src / "one.cu").write_text("")
+    (src / "attention_calls.cpp").write_text("#error no torch headers\n")
+    cc = tmp_path / "nvcc"
+    cc.write_text("#!/bin/sh\nwhile [ $# -gt 0 ]; do [ \"$1\" = -o ] && : > \"$2\"; shift; done\n")
+    cc.chmod(0o755)
+    for name, value in (("CSRC", src), ("BUILD", tmp_path / "_build"), ("LIB", tmp_path / "libsvdq.so"),
+                        ("CALLS_SRC", src / "attention_calls.cpp"), ("INCLUDE", tmp_path / "include")):
+        monkeypatch.setattr(rbuild, name, str(value))
+    monkeypatch.setattr(rbuild, "calls_path", lambda: str(tmp_path / "_calls.so"))
+    monkeypatch.setenv("NVCC", str(cc))
+    return tmp_path
+
+
+def missing_compiler(out):
+    return ["/nowhere/g++", "-o", out]
+
+
+def missing_torch(out):
+    raise ImportError("no torch")
+
+
+@pytest.mark.parametrize("command", [None, missing_compiler, missing_torch])
+def test_the_library_is_built_whatever_becomes_of_the_quick_calls(small_tree, monkeypatch, command):
+    if command is not None:
+        monkeypatch.setattr(rbuild, "calls_command", command)
+    for _ in range(2):                       # the second time only the quick calls are missing
+        with pytest.warns(RuntimeWarning, match="quick calls"):
+            assert rbuild.build() == rbuild.LIB
+        assert os.path.exists(rbuild.LIB) and not os.path.exists(rbuild.calls_path())
+
+
+def test_a_failure_of_the_library_raises(small_tree, monkeypatch):
+    monkeypatch.setattr(rbuild, "calls_command", lambda out: ["touch", out])
+    (small_tree / "nvcc").write_text("#!/bin/sh\necho wrong; exit 1\n")
+    with pytest.raises(RuntimeError, match="wrong"):
+        rbuild.build()
+    assert not os.path.exists(rbuild.LIB)
