@@ -123,11 +123,17 @@ def norm_rope_tolerance(y, magnitude, eps_out):
     return eps_out / 2 * np.abs(y) + 32 * 2.0 ** -24 * magnitude
 
 
-def attention_tolerance(out, spread, reach, dim, keys):
-    """Relative to spread = sum p |v| / sum p: each p rounded to bf16 (2^-8), its score in fp32
+EXP2_CUBIC = 7.5e-5   # of the prompt kernel's cubic for 2^x, fp32 evaluation included
+
+
+def attention_tolerance(out, spread, reach, dim, keys, exp2=EXP2_CUBIC):
+    """Relative to spread = sum p |v| / sum p: each p in fp32 off by the exponential (`exp2`: the
+    prompt kernel takes some from a cubic, the decode kernel none, exp2 = 0), by its score
     (dim products and sums of magnitude at most `reach`, the scaling and the difference to the
-    maximum: (dim + 4) 2^-24 reach, once in p and once in the total), exp2 (2 ulp, in p and in
-    the total: 8 2^-24) and `keys` fp32 additions in both sums; then one rounding of the
-    result to bf16."""
-    rel = 2.0 ** -8 + 2 * (dim + 4) * 2.0 ** -24 * reach + (8 + 2 * keys) * 2.0 ** -24
-    return rel * spread + 2.0 ** -8 * np.abs(out)
+    maximum: (dim + 4) 2^-24 reach) and by 2 ulp of the other exponentials (4 2^-24): all
+    three once in p and once in the total, and `keys` fp32 additions in both sums. Then p rounded to
+    bf16, off by at most 2^-8 / (1 + 2^-8) of it, and the result to bf16, off by 2^-8 of its
+    value, the errors so far included: with those (1 + 2^-8) the rounding of p is 2^-8, and the
+    terms in fp32 are taken (1 + 2^-8)^2 < 1 + 2^-6 times."""
+    fp32 = 2 * exp2 + 2 * (dim + 4) * 2.0 ** -24 * reach + (8 + 2 * keys) * 2.0 ** -24
+    return (2.0 ** -8 + (1 + 2.0 ** -6) * fp32) * spread + 2.0 ** -8 * np.abs(out)
