@@ -492,14 +492,14 @@ def svdq_linear_chain(weights, x: torch.Tensor, biases=None, out_dtype=torch.bfl
     intermediate y is in out_dtype (bf16 by default); ``outs`` may hold
     preallocated outputs, one per linear.
 
-    An entry of ``weights`` that is not a prepared weight is a step between two
-    linears, called with the y before it and returning the x of the next (e.g. an
+    An entry of ``weights`` that can be called (and is no prepared weight) is a step between
+    two linears, called with the y before it and returning the x of the next (e.g. an
     AttentionStep); its entries in ``biases`` and ``outs`` must be None."""
     biases = biases if biases is not None else [None] * len(weights)
     ws = workspace or LinearWorkspace()
     y = x
     for i, (w, b) in enumerate(zip(weights, biases)):
-        if not isinstance(w, PreparedWeight):
+        if callable(w) and not isinstance(w, PreparedWeight):
             if b is not None or (outs is not None and outs[i] is not None):
                 raise ValueError("a step between linears takes no bias and no preallocated output")
             y = w(y)
