@@ -406,7 +406,8 @@ typedef struct svdq_heads {
  *   (a, b) -> amplitude * (a cos - b sin, b cos + a sin)
  * with (a, b) = elements (j, j + rot_dim/2) of the head, or (2j, 2j + 1) when
  * interleaved; elements >= rot_dim pass through. The product p turns[j] is reduced to
- * one turn in fp64, so far positions lose nothing. turns holds the frequencies in
+ * one turn in 64-bit integers, within 2^-32 + |p| 2^-64 of a turn, so far positions lose
+ * nothing before the angle becomes a float. turns holds the frequencies in
  * turns per position (base^(-2j/rot_dim) / (2 pi), scaled for long contexts as the
  * model asks; amplitude is that scaling's attention factor, else 1). */
 typedef struct svdq_rope {
@@ -476,7 +477,9 @@ svdq_status svdq_kv_append(const svdq_kv_cache* cache, svdq_heads k, svdq_heads 
  * lengths, grouped heads, causal or full.
  *   out[t, h] = sum_j p_j v[j, h / g] / sum_j p_j,  p_j = exp(scale q[t, h] . k[j, h / g])
  * over the keys j of t's sequence, g = q.heads / k.heads. Everything is bf16; products
- * and sums are fp32, and p is rounded to bf16 for its product with v.
+ * and sums are fp32, and p is rounded to bf16 for its product with v. What lies outside
+ * a sequence (other sequences, rows of none) changes no bit of its rows in out, unless
+ * it changes how the work is divided.
  *
  *   q          [q_tokens, heads, head_dim];  k, v  [k_tokens, kv_heads, head_dim]
  *              heads a multiple of kv_heads; head_dim a multiple of 8, at most 128

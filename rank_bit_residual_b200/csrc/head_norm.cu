@@ -15,9 +15,10 @@
 // half layouts pass the row through shared memory. A warp takes a token, or a share of its heads:
 // the cosines are the same for all heads, so its lanes compute them once, and each lane
 // keeps what it needs of them in registers while the rows go by, the next ones in flight
-// behind these. Angles are exact to 2^-32 of a turn at any position: a frequency is
-// a 64-bit fraction of a turn, and its integer product with the position wraps at whole
-// turns by itself. Warps wait for nothing but their own loads.
+// behind these. A frequency is a 64-bit fraction of a turn (cut there), and its integer
+// product with the position wraps at whole turns by itself: angles are within 2^-32 + |position| 2^-64
+// of a turn, and are then rounded to the 24 bits of a float (of half a turn at most). Warps
+// wait for nothing but their own loads.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

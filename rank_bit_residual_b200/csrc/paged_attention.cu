@@ -18,6 +18,9 @@
 // to 8 query heads fills the eight columns of m16n8k16; with the queries as rows, half
 // of the 16 rows would be padding for such a group. P^T passes from the accumulator layout
 // of the first product to the operand layout of the second by a transposing register move.
+// P is rounded to bf16 there, because the product takes two operands of one 16-bit type and V is
+// bf16: at most 2^-8 of sum p |v| / sum p, as much as the rounding of the result. The sums of the
+// weights take the unrounded fp32 values.
 //
 // A segment that one block finishes is written at once. Pieces of a segment cut by a
 // block boundary go to the workspace (sums in fp32, maximum, total), with a note of the first

@@ -12,8 +12,13 @@
 // these. (With one buffer of 128 keys, softmax waited for P V and the next S in turn: 3400
 // cycles per 128 keys of both tiles against 2048 of products.)
 //
-// With 128-element heads a tile of 128 keys costs 1024 cycles of products and 1024 of
-// exponentials (16 a cycle), so both bound the kernel.
+// With 128-element heads a row tile and 128 keys cost 1280 cycles of products (S in two parts
+// of 64 keys 768, P V 512) and 1024 of exponentials at 16 a cycle, 768 of them left after the
+// quarter that the FMA pipe takes, so both bound the kernel.
+//
+// P is rounded to bf16 because the product takes two operands of one 16-bit type and V is bf16:
+// at most 2^-8 of sum p |v| / sum p, as much as the rounding of the result. The sums of the
+// weights take the unrounded fp32 values.
 //
 // The maximum is renewed (and O rescaled, by the softmax warps themselves) only when a
 // score passes it by 2^8; P then stays below 2^8, and both sums are fp32. O is at rest for
@@ -28,7 +33,7 @@
 //
 // Few rows over many keys would leave most SMs idle: the keys of an item are then divided
 // among several items, whose unfinished sums a second kernel joins (301 rows over 7501 keys,
-// 48 items: 108 us with one share, 63 with three).
+// 40 items: 102 us with one share, 53 with three).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -863,8 +868,8 @@ PromptPlan plan_prompt(int heads, int kv_heads, int batch, int64_t q_tokens, int
   PromptPlan p;
   // Heads that share their keys lie side by side in a tile, a power of two of them: fewer rows
   // of the sequence then are in it, of which fewer lie behind its end or beside the diagonal
-  // (with two side by side 9 ragged prompts of 32 on 8 heads took 98.7 us instead of 96.5, 1000 sequences
-  // of 30 rows 525 instead of 278 at the time).
+  // (32 on 8 heads, with one, two and all four of a group side by side: 9 ragged prompts 110, 94 and
+  // 92 us, 1000 sequences of 30 rows 883, 458 and 248, 128 of 100 rows 152, 84 and 90).
   const int group = heads / kv_heads;
   for (p.fold = 0; p.fold < kMaxFold && group % (2 << p.fold) == 0;) ++p.fold;
   p.pairs = heads >> p.fold;

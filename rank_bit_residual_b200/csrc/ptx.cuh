@@ -124,7 +124,9 @@ __device__ __forceinline__ bool mbar_wait_soon(uint64_t* bar, uint32_t parity, u
 // Warp-wide wait (call with the warp converged): lane 0 polls the barrier and
 // the result is broadcast, so a waiting warp puts one poller on the
 // shared-memory pipe instead of 32; the warp barrier after the poll orders the
-// other lanes' later reads after lane 0's acquire.
+// other lanes' later reads after lane 0's acquire (of generic writes and of copies that
+// completed on the barrier alike), and brings the lanes together: a shuffle alone does not
+// promise that the .aligned instructions behind it find them converged.
 __device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, unsigned* status,
                                                volatile int* abort,
                                                unsigned long long limit_ns = kWaitLimitNs) {
