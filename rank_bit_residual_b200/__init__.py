@@ -427,7 +427,10 @@ def svdq_quantize_act_noalloc(x: torch.Tensor, scale: torch.Tensor, fmt="int4",
 
 
 class LinearWorkspace:
-    """Reusable scratch for svdq_linear (one per stream in flight)."""
+    """Reusable scratch for svdq_linear and the attention calls (one per stream in flight).
+
+    A call that needs more replaces the buffer. A captured graph keeps the address of the one it
+    was captured with: give a graph a workspace of its own, and no larger call behind the capture."""
 
     def __init__(self):
         self.buf = None
